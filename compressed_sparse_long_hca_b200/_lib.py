@@ -67,6 +67,11 @@ SIGNATURES = {
     "csa_gemm_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
     "csa_gemm_bf16": (_I32, [_P, _I32, _I32, _I32, _P, _I32, _I32, _P, _P, _SZ, _P]),
     "csa_gemm_check_device_error": (_I32, [_P]),
+    "csa_gemm_fp8_weight_bytes": (_SZ, [_I32, _I32, _I32]),
+    "csa_gemm_fp8_quant_weight": (_I32, [_P, _I32, _I32, _I32, _P, _P, _P]),
+    "csa_gemm_fp8_pack_weight": (_I32, [_P, _P, _I32, _I32, _I32, _P, _SZ, _P]),
+    "csa_gemm_fp8_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "csa_gemm_fp8": (_I32, [_P, _I32, _I32, _I32, _P, _I32, _I32, _P, _P, _SZ, _P]),
 }
 
 _lib = None

@@ -7,6 +7,7 @@ dtypes and devices and pass raw pointers.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 
 import numpy as np
 import torch
@@ -645,6 +646,138 @@ class Linear:
     @staticmethod
     def check_device_error(stream=None) -> None:
         check(_lib.load().csa_gemm_check_device_error(_stream(stream)), "gemm device")
+
+
+def _current_device(device: torch.device):
+    """A context in which `device` is the current CUDA device (none when it
+    is already)."""
+    return nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _scratch(nbytes: int, device: torch.device, stream) -> torch.Tensor:
+    """Scratch for one call on `stream`, from the allocator of that stream:
+    calls on different streams, and graphs captured one by one, never share
+    it.  The allocator reuses it only behind the work queued so far."""
+    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+class LinearFP8:
+    """A weight in 8-bit floating point with one power-of-two scale per
+    128 x 128 block, packed once for csa_gemm_fp8: Y[t][o] = sum_k X[t][k]
+    W[o][k], the BF16 tokens quantised inside the call with one scale per 128
+    of a token's values, fp32 accumulation.  Streams half the bytes of Linear
+    and is batch-invariant as it is.
+
+    codes: CUDA tensor [n_out][k_in // groups] of E4M3 codes (float8_e4m3fn,
+    or their bytes as uint8), contiguous; scales: CUDA tensor
+    [ceil(n_out / 128)][ceil(k_in / groups / 128)] of E8M0 scales
+    (float8_e8m0fnu, or biased exponents as uint8: 2^(byte - 127)),
+    contiguous.  With groups > 1 the weight is block diagonal, as Linear's.
+    LinearFP8.quantize makes both from a real weight.  Neither is kept."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, groups: int = 1, stream=None):
+        self.lib = _lib.load()
+        if isinstance(codes, torch.Tensor) and codes.dtype == torch.float8_e4m3fn:
+            codes = codes.view(torch.uint8)
+        if isinstance(scales, torch.Tensor) and scales.dtype == torch.float8_e8m0fnu:
+            scales = scales.view(torch.uint8)
+        _need(codes, torch.uint8, name="codes")
+        if codes.dim() != 2:
+            raise ValueError("codes must be [n_out, k_in // groups]")
+        self.device = codes.device
+        self.groups = int(groups)
+        self.n_out, kg = (int(v) for v in codes.shape)
+        self.k_in = kg * self.groups
+        nbytes = self.lib.csa_gemm_fp8_weight_bytes(self.n_out, self.k_in, self.groups)
+        if nbytes == 0:
+            raise ValueError("invalid GEMM weight shape")
+        _need(scales, torch.uint8, (-(-self.n_out // 128), -(-kg // 128)), "scales")
+        if scales.device != self.device:
+            raise ValueError("codes and scales must be on one device")
+        with _current_device(self.device):
+            self.packed = _scratch(nbytes, self.device, stream)
+            check(self.lib.csa_gemm_fp8_pack_weight(_ptr(codes), _ptr(scales), self.n_out, self.k_in, self.groups,
+                                                    self.packed.data_ptr(), nbytes, _stream(stream)),
+                  "csa_gemm_fp8_pack_weight")
+        self._need_bytes = {}
+
+    @classmethod
+    def quantize(cls, w, groups: int = 1, device: str | torch.device = "cuda", stream=None) -> "LinearFP8":
+        """From a real weight [n_out][k_in // groups] (host array, or a
+        tensor; rounded to BF16 first): E4M3 codes with, per 128 x 128 block,
+        the least power-of-two scale that holds the block."""
+        codes, scales = quantize_fp8_weight(w, device=device, stream=stream)
+        return cls(codes, scales, groups=groups, stream=stream)
+
+    def workspace_bytes(self, n_tok: int) -> int:
+        need = self._need_bytes.get(n_tok)
+        if need is None:
+            with _current_device(self.device):
+                need = int(self.lib.csa_gemm_fp8_workspace_bytes(self.n_out, self.k_in, self.groups, n_tok))
+            self._need_bytes[n_tok] = need
+        return need
+
+    def __call__(self, x: torch.Tensor, outs, workspace: torch.Tensor | None = None, stream=None):
+        """x: CUDA BF16 [n_tok][k_in].  outs: one tensor or a list of CUDA
+        tensors [n_tok][rows_s] (BF16 or fp32, contiguous) whose rows add up
+        to n_out, as Linear's.  Unless `workspace` is given, the call takes
+        scratch of its own from the allocator.  Returns outs."""
+        segs = [outs] if isinstance(outs, torch.Tensor) else outs
+        n = x.shape[0] if x.dim() == 2 else -1
+        _need(x, torch.bfloat16, (n, self.k_in), "x")
+        arr = (_lib.GemmOut * len(segs))()
+        for s, t in enumerate(segs):
+            bf16 = t.dtype == torch.bfloat16
+            _need(t, torch.bfloat16 if bf16 else torch.float32, (n, t.shape[1] if t.dim() == 2 else -1), f"outs[{s}]")
+            if t.device != self.device:
+                raise ValueError("outputs must be on the weight's device")
+            arr[s].rows, arr[s].bf16, arr[s].y = t.shape[1], bf16, t.data_ptr()
+        if x.device != self.device:
+            raise ValueError("x must be on the weight's device")
+        if n == 0:
+            return outs
+        with _current_device(self.device):
+            if workspace is None:
+                workspace = _scratch(self.workspace_bytes(n) + 256, self.device, stream)
+            else:
+                _need(workspace, torch.uint8, name="workspace")
+                if workspace.device != self.device:
+                    raise ValueError("workspace must be on the weight's device")
+            at = workspace.data_ptr()
+            ws = (at + 255) // 256 * 256
+            check(self.lib.csa_gemm_fp8(self.packed.data_ptr(), self.n_out, self.k_in, self.groups, x.data_ptr(), n,
+                                        len(segs), arr, ws, workspace.numel() - (ws - at), _stream(stream)),
+                  "csa_gemm_fp8")
+        return outs
+
+    @staticmethod
+    def check_device_error(stream=None) -> None:
+        check(_lib.load().csa_gemm_check_device_error(_stream(stream)), "gemm device")
+
+
+def quantize_fp8_weight(w, device: str | torch.device = "cuda", stream=None):
+    """E4M3 codes (float8_e4m3fn [n_out, k]) and E8M0 scales (uint8 biased
+    exponents [ceil(n_out / 128), ceil(k / 128)]) of a real weight [n_out, k]
+    (host array or tensor; rounded to BF16 first), through
+    csa_gemm_fp8_quant_weight.  A block with an infinity or a NaN gets the
+    NaN scale (255)."""
+    if not isinstance(w, torch.Tensor):
+        w = torch.from_numpy(np.ascontiguousarray(np.asarray(w, dtype=np.float32)))
+    if w.dim() != 2 or not w.is_floating_point():
+        raise ValueError("w must be a real matrix [n_out, k]")
+    if not w.is_cuda:
+        w = w.to(device)
+    w = w.to(torch.bfloat16).contiguous()
+    n_out, k = (int(v) for v in w.shape)
+    with _current_device(w.device):
+        codes = torch.empty((n_out, k), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((-(-n_out // 128), -(-k // 128)), dtype=torch.uint8, device=w.device)
+        check(_lib.load().csa_gemm_fp8_quant_weight(_ptr(w), n_out, k, 1, _ptr(codes), _ptr(scales), _stream(stream)),
+              "csa_gemm_fp8_quant_weight")
+    return codes.view(torch.float8_e4m3fn), scales
 
 
 class LayerProjections:

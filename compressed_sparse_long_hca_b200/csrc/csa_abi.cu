@@ -54,6 +54,15 @@ void gemm_pack_weight_host(const uint16_t* w, int n_out, int k_in, int groups, u
 cudaError_t launch_gemm_bf16(const void* w_packed, int n_out, int k_in, int groups, const uint16_t* x, int n_tok,
                              const GemmOut& out, void* ws, int sms, cudaStream_t st);
 cudaError_t gemm_read_error(int32_t* code, int32_t* detail, cudaStream_t st);
+size_t fp8_weight_bytes(int n_out, int k_in, int groups);
+size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok, int sms);
+cudaError_t launch_fp8_pack_weight(const uint8_t* codes, const uint8_t* scales, int n_out, int k_in, int groups,
+                                   uint8_t* w, cudaStream_t st);
+cudaError_t launch_fp8_quant_weight(const uint16_t* w, int n_out, int k_in, int groups, uint8_t* codes,
+                                    uint8_t* scales, cudaStream_t st);
+cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int groups, const uint16_t* x, int n_tok,
+                            const GemmOut& out, void* ws, int sms, cudaStream_t st);
+cudaError_t fp8_read_error(int32_t* code, int32_t* detail);
 }  // namespace csa
 
 namespace {
@@ -794,24 +803,31 @@ size_t csa_gemm_workspace_bytes(int32_t n_out, int32_t k_in, int32_t groups, int
   return csa::gemm_workspace_bytes(n_out, k_in, groups, n_tok, sms);
 }
 
+// The output segments of a projection call as the kernels take them.
+static bool gemm_segments(int32_t n_out, int32_t n_seg, const csa_gemm_out* segs, csa::GemmOut* out, std::string* why) {
+  if (n_seg < 1 || n_seg > csa::kGemmMaxSeg || !segs) { *why = "n_seg must be in [1, 8]"; return false; }
+  out->n_seg = n_seg;
+  int64_t rows = 0;
+  for (int s = 0; s < n_seg; ++s) {
+    if (segs[s].rows < 1 || !segs[s].y) { *why = "every output segment needs rows >= 1 and y"; return false; }
+    rows += segs[s].rows;
+    if (rows > n_out) break;
+    out->seg_end[s] = (int)rows;
+    out->y[s] = segs[s].y;
+    if (segs[s].bf16) out->bf16_mask |= 1u << s;
+  }
+  if (rows != n_out) { *why = "the segments' rows must add up to n_out"; return false; }
+  return true;
+}
+
 csa_status csa_gemm_bf16(const void* w_packed, int32_t n_out, int32_t k_in, int32_t groups, const uint16_t* x,
                          int32_t n_tok, int32_t n_seg, const csa_gemm_out* segs, void* workspace,
                          size_t workspace_bytes, csa_stream_t stream) {
   std::string why;
   if (!gemm_shape_ok(n_out, k_in, groups, &why)) return fail(CSA_ERR_ARG, why);
   if (n_tok < 0 || n_tok > csa::gemm_max_tokens()) return fail(CSA_ERR_ARG, "n_tok must be in [0, 256]");
-  if (n_seg < 1 || n_seg > csa::kGemmMaxSeg || !segs) return fail(CSA_ERR_ARG, "n_seg must be in [1, 8]");
   csa::GemmOut out{};
-  out.n_seg = n_seg;
-  int rows = 0;
-  for (int s = 0; s < n_seg; ++s) {
-    if (segs[s].rows < 1 || !segs[s].y) return fail(CSA_ERR_ARG, "every output segment needs rows >= 1 and y");
-    rows += segs[s].rows;
-    out.seg_end[s] = rows;
-    out.y[s] = segs[s].y;
-    if (segs[s].bf16) out.bf16_mask |= 1u << s;
-  }
-  if (rows != n_out) return fail(CSA_ERR_ARG, "the segments' rows must add up to n_out");
+  if (!gemm_segments(n_out, n_seg, segs, &out, &why)) return fail(CSA_ERR_ARG, why);
   if (n_tok == 0) return CSA_OK;
   if (!w_packed || !x || !workspace) return fail(CSA_ERR_ARG, "NULL argument");
   if (reinterpret_cast<uintptr_t>(w_packed) % 16 || reinterpret_cast<uintptr_t>(workspace) % 256)
@@ -826,14 +842,97 @@ csa_status csa_gemm_bf16(const void* w_packed, int32_t n_out, int32_t k_in, int3
   return CSA_OK;
 }
 
+// ---- FP8 projection product
+
+// The shapes of csa_gemm_fp8: those of csa_gemm_bf16, with room for the row
+// tiles and K blocks in a launch grid.
+static bool fp8_shape_ok(int32_t n_out, int32_t k_in, int32_t groups, std::string* why) {
+  if (!gemm_shape_ok(n_out, k_in, groups, why)) return false;
+  if (n_out > 65535 * 128) { *why = "n_out must be <= 65535 * 128"; return false; }
+  return true;
+}
+
+size_t csa_gemm_fp8_weight_bytes(int32_t n_out, int32_t k_in, int32_t groups) {
+  std::string why;
+  if (!fp8_shape_ok(n_out, k_in, groups, &why)) return 0;
+  return csa::fp8_weight_bytes(n_out, k_in, groups);
+}
+
+csa_status csa_gemm_fp8_quant_weight(const uint16_t* w, int32_t n_out, int32_t k_in, int32_t groups, uint8_t* codes,
+                                     uint8_t* scales, csa_stream_t stream) {
+  std::string why;
+  if (!fp8_shape_ok(n_out, k_in, groups, &why)) return fail(CSA_ERR_ARG, why);
+  if (!w || !codes || !scales) return fail(CSA_ERR_ARG, "NULL argument");
+  if (reinterpret_cast<uintptr_t>(w) % 2) return fail(CSA_ERR_ARG, "w must be 2-byte aligned");
+  cudaError_t e = csa::launch_fp8_quant_weight(w, n_out, k_in, groups, codes, scales, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 weight quantisation launch");
+  return CSA_OK;
+}
+
+csa_status csa_gemm_fp8_pack_weight(const uint8_t* codes, const uint8_t* scales, int32_t n_out, int32_t k_in,
+                                    int32_t groups, void* w_dev, size_t bytes, csa_stream_t stream) {
+  std::string why;
+  if (!fp8_shape_ok(n_out, k_in, groups, &why)) return fail(CSA_ERR_ARG, why);
+  if (!codes || !scales || !w_dev || reinterpret_cast<uintptr_t>(w_dev) % 16)
+    return fail(CSA_ERR_ARG, "NULL argument, or w_dev not 16-byte aligned");
+  if (bytes < csa::fp8_weight_bytes(n_out, k_in, groups))
+    return fail(CSA_ERR_CAPACITY, "w_dev smaller than csa_gemm_fp8_weight_bytes");
+  cudaError_t e = csa::launch_fp8_pack_weight(codes, scales, n_out, k_in, groups, static_cast<uint8_t*>(w_dev),
+                                              (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 weight packing launch");
+  return CSA_OK;
+}
+
+size_t csa_gemm_fp8_workspace_bytes(int32_t n_out, int32_t k_in, int32_t groups, int32_t n_tok) {
+  std::string why;
+  if (!fp8_shape_ok(n_out, k_in, groups, &why) || n_tok < 1 || n_tok > CSA_FP8_MAX_TOKENS) return 0;
+  const int sms = sm_count();
+  if (sms <= 0) return 0;
+  return csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok, sms);
+}
+
+csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32_t groups, const uint16_t* x,
+                        int32_t n_tok, int32_t n_seg, const csa_gemm_out* segs, void* workspace,
+                        size_t workspace_bytes, csa_stream_t stream) {
+  std::string why;
+  if (!fp8_shape_ok(n_out, k_in, groups, &why)) return fail(CSA_ERR_ARG, why);
+  if (n_tok < 0 || n_tok > CSA_FP8_MAX_TOKENS) return fail(CSA_ERR_ARG, "n_tok must be in [0, 1048576]");
+  csa::GemmOut out{};
+  if (!gemm_segments(n_out, n_seg, segs, &out, &why)) return fail(CSA_ERR_ARG, why);
+  for (int s = 0; s < n_seg; ++s)
+    if (reinterpret_cast<uintptr_t>(segs[s].y) % (segs[s].bf16 ? 2 : 4))
+      return fail(CSA_ERR_ARG, "an output segment is not aligned to its elements");
+  if (n_tok == 0) return CSA_OK;
+  if (!w_packed || !x || !workspace) return fail(CSA_ERR_ARG, "NULL argument");
+  if (reinterpret_cast<uintptr_t>(x) % 2) return fail(CSA_ERR_ARG, "x must be 2-byte aligned");
+  if (reinterpret_cast<uintptr_t>(w_packed) % 16 || reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(CSA_ERR_ARG, "w_packed must be 16-byte and workspace 256-byte aligned");
+  const int sms = sm_count();
+  if (sms <= 0) return fail(CSA_ERR_CUDA, "cannot query the SM count");
+  if (workspace_bytes < csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok, sms))
+    return fail(CSA_ERR_ARG, "workspace smaller than csa_gemm_fp8_workspace_bytes");
+  cudaError_t e = csa::launch_gemm_fp8(w_packed, n_out, k_in, groups, x, n_tok, out, workspace, sms,
+                                       (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 gemm launch");
+  return CSA_OK;
+}
+
 csa_status csa_gemm_check_device_error(csa_stream_t stream) {
   int32_t code = 0, detail = 0;
   cudaError_t e = csa::gemm_read_error(&code, &detail, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "gemm error word");
-  if (code == 0) return CSA_OK;
   char msg[120];
-  snprintf(msg, sizeof msg, "device: a GEMM pipeline wait gave up (row tile %d)", detail);
-  return fail(CSA_ERR_DEVICE_TIMEOUT, msg);
+  if (code != 0) {
+    snprintf(msg, sizeof msg, "device: a GEMM pipeline wait gave up (row tile %d)", detail);
+    return fail(CSA_ERR_DEVICE_TIMEOUT, msg);
+  }
+  e = csa::fp8_read_error(&code, &detail);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 gemm error word");
+  if (code != 0) {
+    snprintf(msg, sizeof msg, "device: an FP8 GEMM pipeline wait gave up (block %d)", detail);
+    return fail(CSA_ERR_DEVICE_TIMEOUT, msg);
+  }
+  return CSA_OK;
 }
 
 csa_status csa_debug_wait_timeout(csa_cache_t* c, int32_t limit_us, csa_stream_t stream) {

@@ -163,6 +163,18 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, uint32_t a_sf_id, u
   return d;
 }
 
+// Instruction descriptor of kind::mxf8f6f4 with E4M3 operands, both K-major
+// (one E8M0 scale per row and K = 32, fp32 accumulate).
+__device__ __forceinline__ uint32_t idesc_mxf8(int M, int N, uint32_t a_sf_id, uint32_t b_sf_id) {
+  uint32_t d = 0;                      // A and B format E4M3 are 0
+  d |= (b_sf_id & 3u) << 4;
+  d |= (uint32_t)(N >> 3) << 17;
+  d |= 1u << 23;                       // scale type UE8M0
+  d |= (uint32_t)(M >> 4) << 24;
+  d |= (a_sf_id & 3u) << 29;
+  return d;
+}
+
 // Instruction descriptor of kind::f16 with BF16 inputs and fp32 accumulate.
 // a_mn / b_mn select the MN-major (transposed) operand layouts.
 __device__ __forceinline__ uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
@@ -200,6 +212,15 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint6
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p; }"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p; }"
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
       : "memory");
 }

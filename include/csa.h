@@ -528,6 +528,58 @@ csa_status csa_gemm_bf16(const void* w_packed, int32_t n_out, int32_t k_in, int3
                          void* workspace, size_t workspace_bytes, csa_stream_t stream);
 csa_status csa_gemm_check_device_error(csa_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Projection product in 8-bit floating point with a scale per block of 128,
+ * the counterpart of csa_gemm_bf16 that streams half the weight bytes:
+ *   Y[t][o] = sum_b 2^(ex[t][b] + ew[o/128][b]) sum_{c in block b} X8[t][c] W8[o][c]
+ * (E4M3 codes, power-of-two scales, fp32 accumulation).  Blocks are 128
+ * columns of a group, the last one possibly shorter.
+ *
+ * Weights: E4M3 codes [n_out][k_in / groups], row-major, one byte each, and
+ * one E8M0 scale byte (2^(byte - 127); 255 = NaN) per block of 128 rows x 128
+ * columns, [ceil(n_out / 128)][ceil(k_in / groups / 128)].
+ * csa_gemm_fp8_quant_weight makes them from a BF16 weight; the rule is the
+ * one the call applies to the tokens: the least e with
+ * amax <= 448 * 2^e (0 for an empty block, clamped to [-127, 127]), code =
+ * E4M3(x * 2^-e) to nearest even.  A block that holds an infinity or a NaN
+ * gets the NaN scale, so that every output that reads it is NaN.
+ *
+ * Tokens: BF16 rows, quantised inside the call per token and block.
+ *
+ * Batch invariance: as csa_gemm_bf16.  The K order and its cut into parts
+ * depend on the weight's shape and the device's SM count alone, for one
+ * token and for thousands: a token's bits do not depend on its batch.
+ *
+ *   csa_gemm_fp8_weight_bytes   device bytes of a packed weight (0 for a bad
+ *                           shape: groups must divide n_out and k_in, with
+ *                           groups > 1 n_out / groups is a multiple of 128,
+ *                           k_in / groups is a multiple of 8)
+ *   csa_gemm_fp8_quant_weight   device BF16 W -> device codes and scales;
+ *                           asynchronous
+ *   csa_gemm_fp8_pack_weight    device codes and scales -> packed tiles
+ *                           (w_dev 16-byte aligned); asynchronous
+ *   csa_gemm_fp8_workspace_bytes  scratch of one call of n_tok tokens
+ *   csa_gemm_fp8            X device BF16 [n_tok][k_in], 0 <= n_tok <=
+ *                           CSA_FP8_MAX_TOKENS; output segments as
+ *                           csa_gemm_bf16 (y of an fp32 segment 4-byte, of
+ *                           a BF16 segment 2-byte aligned); workspace
+ *                           256-byte aligned, owned by the caller, not used
+ *                           by other work until the call's kernels finish.
+ *                           Asynchronous.
+ * Device errors are read with csa_gemm_check_device_error.
+ * ------------------------------------------------------------------- */
+#define CSA_FP8_MAX_TOKENS 1048576
+
+size_t     csa_gemm_fp8_weight_bytes(int32_t n_out, int32_t k_in, int32_t groups);
+csa_status csa_gemm_fp8_quant_weight(const uint16_t* w, int32_t n_out, int32_t k_in, int32_t groups,
+                                     uint8_t* codes, uint8_t* scales, csa_stream_t stream);
+csa_status csa_gemm_fp8_pack_weight(const uint8_t* codes, const uint8_t* scales, int32_t n_out, int32_t k_in,
+                                    int32_t groups, void* w_dev, size_t bytes, csa_stream_t stream);
+size_t     csa_gemm_fp8_workspace_bytes(int32_t n_out, int32_t k_in, int32_t groups, int32_t n_tok);
+csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32_t groups, const uint16_t* x,
+                        int32_t n_tok, int32_t n_seg, const csa_gemm_out* segs, void* workspace,
+                        size_t workspace_bytes, csa_stream_t stream);
+
 /*
  * Read and clear the device error word (synchronises `stream`).  Returns
  * CSA_OK or the first device error recorded since the last check;

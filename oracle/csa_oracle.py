@@ -378,6 +378,66 @@ def grouped_linear(x, W, groups: int) -> np.ndarray:
 
 
 # ---------------------------------------------------------------------------
+# FP8 projection: E4M3 codes with a power-of-two scale per block of 128
+# columns (tokens: per row; weights: per 128 rows), fp64 sums.
+# ---------------------------------------------------------------------------
+
+def fp8_block_exponent(amax: float) -> int:
+    """The least e in [-127, 127] with amax <= 448 * 2^e; 0 for an empty block."""
+    if amax == 0.0:
+        return 0
+    e = -127
+    while e < 127 and amax > math.ldexp(E4M3_MAX, e):
+        e += 1
+    return e
+
+
+def fp8_quantize_blocks(x, groups: int = 1, rows: int = 1):
+    """Codes (uint8, as x) and E8M0 bytes [ceil(n / rows), groups * blocks] of
+    real values x [n, groups * kg]: blocks of `rows` rows x 128 columns of a
+    group.  A block with a value that is not finite: codes 0, scale byte 255."""
+    x = np.asarray(x, np.float64)
+    n, k = x.shape
+    kg = k // groups
+    codes = np.zeros((n, k), np.uint8)
+    scales = []
+    for r0 in range(0, n, rows):
+        line = []
+        for g in range(groups):
+            for c0 in range(0, kg, 128):
+                at = (slice(r0, r0 + rows), slice(g * kg + c0, g * kg + min(c0 + 128, kg)))
+                b = x[at]
+                if not np.isfinite(b).all():
+                    line.append(255)
+                    continue
+                e = fp8_block_exponent(float(np.abs(b).max()))
+                codes[at] = e4m3_code(np.ldexp(b, -e))
+                line.append(e + 127)
+        scales.append(line)
+    return codes, np.asarray(scales, np.uint8)
+
+
+def fp8_dequantize_blocks(codes, scales, groups: int = 1, rows: int = 1) -> np.ndarray:
+    """fp64 values of fp8_quantize_blocks' codes and scales (byte 255: NaN)."""
+    codes = np.asarray(codes, np.uint8)
+    n, k = codes.shape
+    kg = k // groups
+    nb = -(-kg // 128)
+    s = np.where(np.asarray(scales) == 255, np.nan, np.exp2(np.asarray(scales, np.float64) - 127))
+    col = np.concatenate([g * nb + np.arange(kg) // 128 for g in range(groups)])
+    return e4m3_value(codes) * s[np.arange(n) // rows][:, col]
+
+
+def fp8_linear(x, codes, scales, groups: int = 1) -> np.ndarray:
+    """The FP8 projection of BF16-representable tokens x [n, k] by a weight of
+    codes [n_out, k / groups] and scales [ceil(n_out / 128), blocks]."""
+    xc, xs = fp8_quantize_blocks(x, groups=groups)
+    xd = fp8_dequantize_blocks(xc, xs, groups=groups)
+    wd = fp8_dequantize_blocks(codes, scales, rows=128)
+    return grouped_linear(xd, wd, groups)
+
+
+# ---------------------------------------------------------------------------
 # Lightning indexer.  [V4-来了] section "CSA——压缩稀疏注意力": the query's hidden
 # state is projected down and up to multi-head index queries, passed through
 # ReLU and scored against the compressed index keys.  Reading: the score is

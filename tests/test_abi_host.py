@@ -158,3 +158,47 @@ def test_gemm_shapes_and_argument_errors_on_the_host(cuda_lib):
     assert g(P, 256, 64, 1, P, 0, 2, segs, P, 1 << 30, None) == 0     # no tokens: nothing to do
     seg[1].y = None
     assert g(P, 256, 64, 1, P, 4, 2, segs, P, 1 << 30, None) == -1    # a segment without an output
+
+
+def test_fp8_gemm_shapes_and_argument_errors_on_the_host(cuda_lib):
+    """The FP8 product's size function and argument checks run on the host:
+    packed bytes are 16 KB tiles of 128 x 128 codes and 512 bytes of scales
+    per row tile and four blocks; every bad argument comes back before any
+    launch (the pointers below are never touched)."""
+    wb = cuda_lib.csa_gemm_fp8_weight_bytes
+    assert wb(300, 1000, 1) == 3 * (8 * 16384 + 2 * 512)
+    assert wb(16 * 128, 16 * 64, 16) == 16 * (16384 + 512)
+    for bad in ((0, 64, 1), (256, 0, 1), (256, 64, 0), (256, 63, 1), (300, 64, 2), (256, 96, 3), (65536 * 128, 64, 1)):
+        assert wb(*bad) == 0, bad
+    P = 0x10000
+    seg = (_lib.GemmOut * 2)()
+    seg[0].rows, seg[0].bf16, seg[0].y = 100, 1, P
+    seg[1].rows, seg[1].bf16, seg[1].y = 156, 0, P
+    segs = ctypes.cast(seg, ctypes.c_void_p)
+    g = cuda_lib.csa_gemm_fp8
+    cases = [
+        ((P, 256, 63, 1, P, 4, 2, segs, P, 1 << 30, None), b"multiple of 8"),
+        ((P, 256, 64, 1, P, -1, 2, segs, P, 1 << 30, None), b"n_tok"),
+        ((P, 256, 64, 1, P, (1 << 20) + 1, 2, segs, P, 1 << 30, None), b"n_tok"),
+        ((P, 256, 64, 1, P, 4, 0, segs, P, 1 << 30, None), b"n_seg"),
+        ((P, 256, 64, 1, P, 4, 9, segs, P, 1 << 30, None), b"n_seg"),
+        ((P, 300, 64, 1, P, 4, 2, segs, P, 1 << 30, None), b"add up"),
+        ((P, 100, 64, 1, P, 4, 2, segs, P, 1 << 30, None), b"add up"),
+        ((None, 256, 64, 1, P, 4, 2, segs, P, 1 << 30, None), b"NULL"),
+        ((P, 256, 64, 1, None, 4, 2, segs, P, 1 << 30, None), b"NULL"),
+        ((P, 256, 64, 1, P + 1, 4, 2, segs, P, 1 << 30, None), b"aligned"),
+        ((P, 256, 64, 1, P, 4, 2, segs, P + 16, 1 << 30, None), b"aligned"),
+        ((P + 8, 256, 64, 1, P, 4, 2, segs, P, 1 << 30, None), b"aligned"),
+    ]
+    for args, msg in cases:
+        assert g(*args) == -1, args
+        assert msg in cuda_lib.csa_last_error(), (args, cuda_lib.csa_last_error())
+    assert g(P, 256, 64, 1, P, 0, 2, segs, P, 1 << 30, None) == 0     # no tokens: nothing to do
+    seg[1].y = P + 2
+    assert g(P, 256, 64, 1, P, 4, 2, segs, P, 1 << 30, None) == -1    # an fp32 segment off its elements
+    assert cuda_lib.csa_gemm_fp8_quant_weight(None, 256, 64, 1, P, P, None) == -1
+    assert cuda_lib.csa_gemm_fp8_quant_weight(P, 256, 60, 1, P, P, None) == -1
+    assert cuda_lib.csa_gemm_fp8_pack_weight(P, P, 256, 64, 1, P + 4, 1 << 30, None) == -1
+    assert cuda_lib.csa_gemm_fp8_pack_weight(P, P, 256, 64, 1, P, 100, None) == -2
+    assert cuda_lib.csa_gemm_fp8_workspace_bytes(256, 64, 1, 0) == 0
+    assert cuda_lib.csa_gemm_fp8_workspace_bytes(256, 64, 1, (1 << 20) + 1) == 0
