@@ -15,13 +15,21 @@ CSA_OK = 0
 STATUS_NAMES = {0: "CSA_OK", -1: "CSA_ERR_ARG", -2: "CSA_ERR_CAPACITY", -3: "CSA_ERR_CUDA",
                 -4: "CSA_ERR_DEVICE_TIMEOUT", -5: "CSA_ERR_DEVICE_BOUNDS"}
 VARIANT_AUTO, VARIANT_HIGH_OCC, VARIANT_LOW_OCC = 0, 1, 2
-ATTN_STATE_READY = 0x100        # flag OR-ed into csa_hca_decode_attn's variant
+ATTN_STATE_READY = 0x100        # flags OR-ed into csa_hca_decode_attn's variant
+ATTN_Q_ROTATED = 0x200
 REGION_KV, REGION_INDEX, REGION_WINDOW = 0, 1, 2
 FMT_MIXED, FMT_F32 = 0, 1
 
 
 class GemmOut(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("bf16", ctypes.c_int32), ("y", ctypes.c_void_p)]
+
+
+class HeadNormPart(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("f32", ctypes.c_int32), ("rotate", ctypes.c_int32)]
 
 
 class CsaCfg(ctypes.Structure):
@@ -71,6 +79,7 @@ SIGNATURES = {
     "csa_gemm_fp8_quant_weight": (_I32, [_P, _I32, _I32, _I32, _P, _P, _P]),
     "csa_gemm_fp8_pack_weight": (_I32, [_P, _P, _I32, _I32, _I32, _P, _SZ, _P]),
     "csa_gemm_fp8_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "csa_head_norm": (_I32, [_I64, _I32, _I32, ctypes.c_double, _P, _P, _P, _P, _P]),
     "csa_gemm_fp8": (_I32, [_P, _I32, _I32, _I32, _P, _I32, _I32, _P, _P, _SZ, _P]),
 }
 

@@ -7,6 +7,7 @@ dtypes and devices and pass raw pointers.
 from __future__ import annotations
 
 import ctypes
+import struct
 from contextlib import nullcontext
 
 import numpy as np
@@ -16,7 +17,7 @@ from . import _lib
 from ._lib import CsaCfg, check
 
 VARIANTS = {"auto": _lib.VARIANT_AUTO, "high": _lib.VARIANT_HIGH_OCC, "low": _lib.VARIANT_LOW_OCC}
-STATE_READY = _lib.ATTN_STATE_READY
+STATE_READY, Q_ROTATED = _lib.ATTN_STATE_READY, _lib.ATTN_Q_ROTATED
 FORMATS = {"mixed": _lib.FMT_MIXED, "f32": _lib.FMT_F32}
 
 
@@ -174,13 +175,15 @@ class Cache:
 
     def decode_attn(self, layer: int, req_ids, q, topk_idx, sink, out, scale=None,
                     variant="auto", stream=None, workspace: torch.Tensor | None = None,
-                    state_ready: bool = False) -> None:
+                    state_ready: bool = False, q_rotated: bool = False) -> None:
         """Attention of each query over its rows.  The split (low-occupancy)
         launch needs scratch; unless `workspace` is given, a buffer owned by
         this Cache object is grown to the size the library asks for.
         state_ready (CSA_ATTN_STATE_READY): the call directly follows this
         step's index_topk on the stream, so the lengths, window rows and q
-        may be read before that kernel ends."""
+        may be read before that kernel ends.
+        q_rotated (CSA_ATTN_Q_ROTATED): q's RoPE dims are rotated already
+        (HeadNorm)."""
         n = req_ids.numel()
         _need(req_ids, torch.int32, name="req_ids")
         _need(q, self.qdtype, (n, self.H, self.D), "q")
@@ -199,7 +202,7 @@ class Cache:
                 workspace = self._workspace(need, q.device)
             _need(workspace, torch.uint8, name="workspace")
             ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
-        flags = STATE_READY if state_ready else 0
+        flags = (STATE_READY if state_ready else 0) | (Q_ROTATED if q_rotated else 0)
         check(self.lib.csa_hca_decode_attn(self.handle, layer, n, _ptr(req_ids), _ptr(q), _ptr(topk_idx),
                                            k, _ptr(sink), scale, _ptr(out), ws_ptr, ws_bytes,
                                            VARIANTS[variant] | flags, _stream(stream)), "csa_hca_decode_attn")
@@ -209,7 +212,7 @@ class Cache:
 
     def prefill_chunk(self, layer: int, req_ids, kv_cand, kv_gate, idx_cand, idx_gate, q, q_idx, w, k: int,
                       sink, out, topk_out=None, scale=None, variant="auto", stream=None,
-                      workspace: torch.Tensor | None = None) -> None:
+                      workspace: torch.Tensor | None = None, q_rotated: bool = False) -> None:
         """A chunk of n_tok (1 .. 128) new tokens per request, each also a
         query with causal visibility (csa_prefill_chunk): the tokens are
         appended, and query j of request b (at position len - n_tok + j)
@@ -217,7 +220,8 @@ class Cache:
         [n, n_tok, D] fp32; idx_cand, idx_gate [n, n_tok, d_I] fp32, q_idx
         [n, n_tok, H_I, d_I] and w [n, n_tok, H_I] fp32 (CSA layers, else
         None); q and out [n, n_tok, H, D] (BF16, fp32 in the fp32 format);
-        topk_out [n, n_tok, k] int32 or None.  Unless `workspace` is given, a
+        topk_out [n, n_tok, k] int32 or None; q_rotated: q's RoPE dims are
+        rotated already (HeadNorm).  Unless `workspace` is given, a
         buffer owned by this Cache object is grown to the size the library
         asks for."""
         n = req_ids.numel()
@@ -255,7 +259,8 @@ class Cache:
         check(self.lib.csa_prefill_chunk(self.handle, layer, n, _ptr(req_ids), n_tok, _ptr(kv_cand), _ptr(kv_gate),
                                          _ptr(idx_cand), _ptr(idx_gate), _ptr(q), _ptr(q_idx), _ptr(w), k,
                                          _ptr(sink), scale, _ptr(out), _ptr(topk_out), ws_ptr, ws_bytes,
-                                         VARIANTS[variant], _stream(stream)), "csa_prefill_chunk")
+                                         VARIANTS[variant] | (Q_ROTATED if q_rotated else 0), _stream(stream)),
+              "csa_prefill_chunk")
 
     def check_device_error(self, stream=None) -> None:
         check(self.lib.csa_check_device_error(self.handle, _stream(stream)), "device")
@@ -780,6 +785,94 @@ def quantize_fp8_weight(w, device: str | torch.device = "cuda", stream=None):
     return codes.view(torch.float8_e4m3fn), scales
 
 
+class HeadNorm:
+    """RMS norm of every query head and key head with the partial RoPE, in one
+    launch (csa_head_norm): y = w * x / sqrt(mean(x^2) + eps), the pairs
+    (2i, 2i+1) of a query's last `rope` dims then rotated by position *
+    rope_base^(-2i / rope) (keys too with rotate_k).
+
+    dim: even, at most 1024; rope: even, at most dim.  q_weight, k_weight:
+    [dim] values (host array or tensor, kept in fp32), None for ones.  The
+    rotated queries go to the attention with q_rotated=True."""
+
+    def __init__(self, dim: int, rope: int, q_weight=None, k_weight=None, eps: float = 1e-6, rope_base: float = 10000.0,
+                 rotate_k: bool = False, device: str | torch.device = "cuda"):
+        self.lib = _lib.load()
+        self.dim, self.rope, self.eps, self.rotate_k = int(dim), int(rope), float(eps), bool(rotate_k)
+        if not 2 <= self.dim <= 1024 or self.dim % 2:
+            raise ValueError("dim must be even, in [2, 1024]")
+        if not 0 <= self.rope <= self.dim or self.rope % 2:
+            raise ValueError("rope must be even, in [0, dim]")
+        if not 0.0 <= self.eps <= 1e30:
+            raise ValueError("eps must be in [0, 1e30]")
+        if not 1.0 < float(rope_base) < float("inf"):
+            raise ValueError("rope_base must be > 1")
+
+        def weight(w, name):
+            if w is None:
+                return None
+            w = torch.as_tensor(w).detach().to(device=device, dtype=torch.float32, copy=True).contiguous()
+            if tuple(w.shape) != (self.dim,):
+                raise ValueError(f"{name} must have shape ({self.dim},), got {tuple(w.shape)}")
+            return w
+
+        self.q_weight, self.k_weight = weight(q_weight, "q_weight"), weight(k_weight, "k_weight")
+        theta = float(rope_base) ** (-2.0 * np.arange(self.rope // 2, dtype=np.float64) / max(self.rope, 1))
+        self.theta = torch.from_numpy(theta).to(device)
+        self.device = self.theta.device
+
+    def _part(self, x, y, weight, rotate, n, name):
+        """The packed csa_head_norm_part of heads x and their output y."""
+        if not isinstance(x, torch.Tensor) or not isinstance(y, torch.Tensor) or x.device != self.device \
+                or y.device != self.device:
+            raise ValueError(f"{name} and {name}_out must be tensors on {self.device}")
+        dt = x.dtype
+        if dt != torch.bfloat16 and dt != torch.float32:
+            raise ValueError(f"{name} must be BF16 or fp32")
+        if x.dim() != 3 or x.shape[0] != n or x.shape[2] != self.dim:
+            raise ValueError(f"{name} must have shape ({n}, heads, {self.dim}), got {tuple(x.shape)}")
+        if y.dtype != dt or y.shape != x.shape:
+            raise ValueError(f"{name}_out must have {name}'s type and shape")
+        (xt, xh, xd), (yt, yh, yd) = x.stride(), y.stride()
+        if (xd != 1 or yd != 1) and x.numel():
+            raise ValueError(f"the dims of {name} and {name}_out must be contiguous")
+        return _HEAD_NORM_PART.pack(x.data_ptr(), y.data_ptr(), 0 if weight is None else weight.data_ptr(), xt, xh, yt, yh,
+                                    x.shape[1], dt == torch.float32, rotate)
+
+    def __call__(self, positions, q, q_out=None, k=None, k_out=None, stream=None):
+        """q: CUDA BF16 or fp32 [n, heads, dim], k: the same or None (its own
+        type and number of heads); any token and head strides, dims
+        contiguous.  q_out, k_out: outputs of the same type and shape (other
+        strides are fine), None for in place; an output is its input or does
+        not overlap any.  positions: CUDA int64 [n], the tokens' positions
+        (None when nothing is rotated).  Returns (q_out, k_out)."""
+        n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else -1
+        q_out = q if q_out is None else q_out
+        k_out = k if k_out is None else k_out
+        part = self._part(q, q_out, self.q_weight, self.rope > 0, n, "q")
+        k_part = None if k is None else self._part(k, k_out, self.k_weight, self.rotate_k and self.rope > 0, n, "k")
+        pos = None
+        if positions is not None or self.rope:
+            _need(positions, torch.int64, (n,), "positions")
+            if positions.device != self.device:
+                raise ValueError(f"positions must be on {self.device}")
+            pos = positions.data_ptr()
+        with _current_device(self.device):
+            check(self.lib.csa_head_norm(n, self.dim, self.rope, self.eps, pos, self.theta.data_ptr(), part, k_part,
+                                         _stream(stream)), "csa_head_norm")
+        return q_out, k_out
+
+
+_HEAD_NORM_PART = struct.Struct("@PPPqqqqiii4x")     # csa_head_norm_part
+
+
+def _projection(fmt: str):
+    """The maker of a packed projection weight in a format."""
+    if fmt not in ("bf16", "fp8"):
+        raise ValueError("fmt must be 'bf16' or 'fp8'")
+    return Linear if fmt == "bf16" else LinearFP8.quantize
+
+
 class LayerProjections:
     """The projections that feed one layer's decode step, from the token's
     hidden state h (BF16 [n, d]) through the batch-invariant GEMM:
@@ -791,20 +884,31 @@ class LayerProjections:
       second call, [W_uq; (W_uqI)] on c_q:
         q [n, H, D] BF16 (before RoPE), on a CSA layer q_I [n, H_I, d_I] fp32.
 
-    Weights are host arrays [out, in] (rounded to BF16 when packed)."""
+    Weights are host arrays [out, in] (rounded to BF16 when packed).  fmt:
+    "bf16" (Linear) or "fp8" (LinearFP8: half the weight bytes; the blocks of
+    128 rows are those of the two fused weights).  norm: a HeadNorm of dim D
+    that is applied in place after the products, to every head of q (with its
+    rotation) and to c; the attention then takes q with q_rotated=True (when
+    the norm's rope is not 0)."""
 
     def __init__(self, *, csa: bool, W_c, W_z, W_dq, W_uq, W_cI=None, W_zI=None, W_w=None, W_uqI=None,
-                 device: str | torch.device = "cuda"):
+                 device: str | torch.device = "cuda", fmt: str = "bf16", norm: HeadNorm | None = None):
+        make = _projection(fmt)
+        self.norm = norm
+        if norm is not None and norm.dim != W_c.shape[0]:
+            raise ValueError(f"norm must have dim {W_c.shape[0]}, got {norm.dim}")
+        if norm is not None and norm.rotate_k:
+            raise ValueError("c is rotated by the append, not by the norm (rotate_k must be False)")
         self.csa = bool(csa)
         self.D = W_c.shape[0]
         self.d = W_c.shape[1]
         self.d_c = W_dq.shape[0]
         first = [W_c, W_z] + ([W_cI, W_zI, W_w] if csa else []) + [W_dq]
         self.rows1 = [int(w.shape[0]) for w in first]
-        self.W1 = Linear(np.concatenate([np.asarray(w, np.float32) for w in first]), device=device)
+        self.W1 = make(np.concatenate([np.asarray(w, np.float32) for w in first]), device=device)
         second = [W_uq] + ([W_uqI] if csa else [])
         self.rows2 = [int(w.shape[0]) for w in second]
-        self.W2 = Linear(np.concatenate([np.asarray(w, np.float32) for w in second]), device=device)
+        self.W2 = make(np.concatenate([np.asarray(w, np.float32) for w in second]), device=device)
         self.d_I = int(W_cI.shape[0]) if csa else 0
         self.H_I = int(W_w.shape[0]) if csa else 0
         self.HD = int(W_uq.shape[0])
@@ -822,7 +926,9 @@ class LayerProjections:
                      q_idx=torch.empty((n, self.H_I, self.rows2[1] // self.H_I), dtype=f32, device=device))
         return o
 
-    def __call__(self, h: torch.Tensor, outs: dict, stream=None) -> dict:
+    def __call__(self, h: torch.Tensor, outs: dict, stream=None, positions: torch.Tensor | None = None) -> dict:
+        """positions: CUDA int64 [n], the tokens' positions (with a norm that
+        rotates)."""
         n = h.shape[0]
         seg1 = [outs["c"].view(n, -1), outs["z"].view(n, -1)]
         if self.csa:
@@ -831,6 +937,8 @@ class LayerProjections:
         self.W1(h, seg1, stream=stream)
         seg2 = [outs["q"].view(n, -1)] + ([outs["q_idx"].view(n, -1)] if self.csa else [])
         self.W2(outs["c_q"], seg2, stream=stream)
+        if self.norm is not None:
+            self.norm(positions, outs["q"], None, outs["c"], None, stream=stream)
         return outs
 
 
@@ -839,12 +947,14 @@ class OutputProjection:
     output (BF16 [n, H, D]) is projected per group of H / groups heads by a
     block-diagonal weight W_g [groups * d_g, (H / groups) * D] to a BF16
     intermediate [n, groups * d_g], then to the model width by W_o
-    [d_model, groups * d_g] (fp32 output [n, d_model])."""
+    [d_model, groups * d_g] (fp32 output [n, d_model]).  fmt: "bf16" (Linear)
+    or "fp8" (LinearFP8)."""
 
-    def __init__(self, W_g, W_o, groups: int, device: str | torch.device = "cuda"):
+    def __init__(self, W_g, W_o, groups: int, device: str | torch.device = "cuda", fmt: str = "bf16"):
+        make = _projection(fmt)
         self.groups = int(groups)
-        self.Wg = Linear(W_g, groups=self.groups, device=device)
-        self.Wo = Linear(W_o, device=device)
+        self.Wg = make(W_g, groups=self.groups, device=device)
+        self.Wo = make(W_o, device=device)
 
     def __call__(self, attn_out: torch.Tensor, mid: torch.Tensor, out: torch.Tensor, stream=None) -> torch.Tensor:
         n = attn_out.shape[0]

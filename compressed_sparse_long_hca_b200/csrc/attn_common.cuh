@@ -66,6 +66,7 @@ struct AttnArgs {
   // (one CTA per chunk) and fold the chunks' partials through distributed
   // shared memory instead of the workspace and attn_fold_kernel
   int cluster_fold;
+  int q_rotated;      // q's RoPE dims are rotated already: taken as they are
 };
 
 struct QueryGeom {

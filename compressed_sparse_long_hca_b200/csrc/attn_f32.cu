@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kF32Threads) attn_f32_kernel(AttnArgs a) {
   }
   if (tid < kF32Heads) { m_r[tid] = -INFINITY; l_r[tid] = 0.f; m_tot[tid] = -INFINITY; l_tot[tid] = 0.f; }
   __syncthreads();
-  for (int x = tid; x < kF32Heads * (R / 2); x += kF32Threads) {
+  for (int x = tid; x < (a.q_rotated ? 0 : kF32Heads * (R / 2)); x += kF32Threads) {
     const int hh = x / (R / 2), p = x % (R / 2);
     rope_pair(qs[hh * QS + D - R + 2 * p], qs[hh * QS + D - R + 2 * p + 1], L.theta()[p], g.t);
   }
@@ -295,10 +295,10 @@ __global__ void __launch_bounds__(kF32Threads) attn_f32_kernel(AttnArgs a) {
 
 cudaError_t launch_attn_f32(const Layout& L, int layer, int n, const int32_t* req_ids, const float* q,
                             const int32_t* topk, int k, const float* sink, float scale, float* out, void* ws,
-                            cudaStream_t st, int q_per_req, const char* win_snap) {
+                            cudaStream_t st, int q_per_req, const char* win_snap, bool q_rotated) {
   const size_t sm = (size_t)f32_smem(L.D).total;
   AttnArgs a{L, layer, n, req_ids, q, topk, k, sink, scale, out, kF32Heads, nullptr, nullptr, 0, 1, 0,
-             q_per_req, win_snap};
+             q_per_req, win_snap, 0, q_rotated ? 1 : 0};
   const int n_hg = (L.H + kF32Heads - 1) / kF32Heads;
   if (ws == nullptr) {
     cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);

@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attn_tc_kernel(AttnArgs a) {
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();                                      // every thread's query copies have landed
-  for (int x = tid; x < G * (R / 2); x += kAttThreads) {
+  for (int x = tid; x < (a.q_rotated ? 0 : G * (R / 2)); x += kAttThreads) {
     // RoPE dims of the query: rotate the BF16 input at t, round to BF16
     const int hh = x / (R / 2), p = x % (R / 2);
     const int d = dmain + 2 * p;
@@ -993,12 +993,13 @@ static cudaError_t cluster_fold_capacity(int C, size_t smem, int* out) {
 
 cudaError_t launch_attn_tc(const Layout& L, int layer, int n, const int32_t* req_ids, const uint16_t* q,
                            const int32_t* topk, int k, const float* sink, float scale, uint16_t* out, int G,
-                           void* ws, cudaStream_t st, bool state_ready, int q_per_req, const char* win_snap) {
+                           void* ws, cudaStream_t st, bool state_ready, int q_per_req, const char* win_snap,
+                           bool q_rotated) {
   const size_t sm = attn_tc_smem_bytes(L.D, G);
   if (sm > 227 * 1024) return cudaErrorInvalidValue;
   const bool split = ws != nullptr;
   AttnArgs a{L, layer, n, req_ids, q, topk, k, sink, scale, out, G, nullptr, nullptr, 0, 0, state_ready ? 1 : 0,
-             q_per_req, win_snap};
+             q_per_req, win_snap, 0, q_rotated ? 1 : 0};
   const int n_hg = (L.H + G - 1) / G;
   // programmatic dependent launch: the kernel may start before the previous
   // grid on the stream ends and waits for it (griddepcontrol) where it must

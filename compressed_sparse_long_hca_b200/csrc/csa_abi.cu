@@ -12,6 +12,7 @@
 
 #include "csa.h"
 #include "gemm_out.cuh"
+#include "head_norm.cuh"
 #include "layout.cuh"
 
 namespace csa {
@@ -27,7 +28,7 @@ cudaError_t launch_topk(const float* scores, int64_t ld, const int32_t* n_valid,
 cudaError_t launch_attn_tc(const Layout& L, int layer, int n, const int32_t* req_ids, const uint16_t* q,
                            const int32_t* topk, int k, const float* sink, float scale, uint16_t* out, int G,
                            void* ws, cudaStream_t st, bool state_ready = false, int q_per_req = 0,
-                           const char* win_snap = nullptr);
+                           const char* win_snap = nullptr, bool q_rotated = false);
 size_t attn_workspace_bytes(const Layout& L, int layer, int n, int k);
 size_t attn_noalloc_scratch_bytes();
 cudaError_t attn_noalloc_scratch(void** out);
@@ -41,7 +42,8 @@ cudaError_t launch_index_f32(const Layout& L, int layer, int n, const int32_t* r
                              cudaStream_t st, int q_per_req = 0);
 cudaError_t launch_attn_f32(const Layout& L, int layer, int n, const int32_t* req_ids, const float* q,
                             const int32_t* topk, int k, const float* sink, float scale, float* out, void* ws,
-                            cudaStream_t st, int q_per_req = 0, const char* win_snap = nullptr);
+                            cudaStream_t st, int q_per_req = 0, const char* win_snap = nullptr,
+                            bool q_rotated = false);
 cudaError_t launch_chunk_prep(const Layout& L, int layer, int n, const int32_t* req_ids, int n_tok, int32_t* req_exp,
                               char* snap, cudaStream_t st);
 cudaError_t launch_copy16(const void* src, void* dst, size_t bytes, cudaStream_t st);
@@ -63,6 +65,8 @@ cudaError_t launch_fp8_quant_weight(const uint16_t* w, int n_out, int k_in, int 
 cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int groups, const uint16_t* x, int n_tok,
                             const GemmOut& out, void* ws, int sms, cudaStream_t st);
 cudaError_t fp8_read_error(int32_t* code, int32_t* detail);
+int head_norm_max_dim();
+cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st);
 }  // namespace csa
 
 namespace {
@@ -437,7 +441,8 @@ static csa_status decode_attn_impl(const csa_cache_t* c, int32_t layer, int32_t 
                                    csa_variant variant_flags, csa_stream_t stream, ChunkQ cq) {
   const int flags = (int)variant_flags & ~0xFF;
   const csa_variant variant = (csa_variant)((int)variant_flags & 0xFF);
-  if (flags & ~CSA_ATTN_STATE_READY) return fail(CSA_ERR_ARG, "unknown variant flag");
+  if (flags & ~(CSA_ATTN_STATE_READY | CSA_ATTN_Q_ROTATED)) return fail(CSA_ERR_ARG, "unknown variant flag");
+  const bool q_rotated = (flags & CSA_ATTN_Q_ROTATED) != 0;
   if (!layer_ok(c, layer)) return fail(CSA_ERR_ARG, "bad layer");
   if (n < 0 || n > 65535) return fail(CSA_ERR_ARG, "n must be in [0, 65535]");
   if (n == 0) return CSA_OK;
@@ -464,10 +469,11 @@ static csa_status decode_attn_impl(const csa_cache_t* c, int32_t layer, int32_t 
       c->L.fmt == csa::kFmtF32
           ? csa::launch_attn_f32(c->L, layer, n, req_ids, static_cast<const float*>(q), topk_idx, kk, sink, scale,
                                  static_cast<float*>(out), split ? workspace : nullptr, (cudaStream_t)stream,
-                                 cq.q_per_req, cq.snap)
+                                 cq.q_per_req, cq.snap, q_rotated)
           : csa::launch_attn_tc(c->L, layer, n, req_ids, static_cast<const uint16_t*>(q), topk_idx, kk, sink,
                                 scale, static_cast<uint16_t*>(out), G, split ? workspace : nullptr,
-                                (cudaStream_t)stream, (flags & CSA_ATTN_STATE_READY) != 0, cq.q_per_req, cq.snap);
+                                (cudaStream_t)stream, (flags & CSA_ATTN_STATE_READY) != 0, cq.q_per_req, cq.snap,
+                                q_rotated);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return CSA_OK;
 }
@@ -718,6 +724,7 @@ bool chunk_shape_ok(const csa_cache* c, int32_t layer, int32_t n, int32_t n_tok,
 size_t csa_prefill_workspace_bytes(const csa_cache_t* c, int32_t layer, int32_t n, int32_t n_tok, int32_t k,
                                    csa_variant variant) {
   std::string why;
+  variant = (csa_variant)((int)variant & ~CSA_ATTN_Q_ROTATED);
   if (!chunk_shape_ok(c, layer, n, n_tok, k, variant, &why)) return 0;
   return (size_t)chunk_layout(c, layer, n, n_tok, layer < c->L.n_csa ? k : 0, variant).total;
 }
@@ -726,8 +733,9 @@ csa_status csa_prefill_chunk(csa_cache_t* c, int32_t layer, int32_t n, const int
                              const float* kv_cand, const float* kv_gate, const float* idx_cand,
                              const float* idx_gate, const void* q, const float* q_idx, const float* w, int32_t k,
                              const float* sink, float scale, void* out, int32_t* topk_out, void* workspace,
-                             size_t workspace_bytes, csa_variant variant, csa_stream_t stream) {
+                             size_t workspace_bytes, csa_variant variant_flags, csa_stream_t stream) {
   std::string why;
+  const csa_variant variant = (csa_variant)((int)variant_flags & ~CSA_ATTN_Q_ROTATED);
   if (!chunk_shape_ok(c, layer, n, n_tok, k, variant, &why)) return fail(CSA_ERR_ARG, why);
   const bool csa = layer < c->L.n_csa;
   if (!req_ids || !kv_cand || !kv_gate || !q || !sink || !out || !workspace) return fail(CSA_ERR_ARG, "NULL argument");
@@ -756,7 +764,7 @@ csa_status csa_prefill_chunk(csa_cache_t* c, int32_t layer, int32_t n, const int
     if (r != CSA_OK) return r;
   }
   return decode_attn_impl(c, layer, Q, req_exp, q, idx, kk, sink, scale, out, cl.ws_bytes ? ws + cl.ws : nullptr,
-                          cl.ws_bytes, variant, stream, cq);
+                          cl.ws_bytes, variant_flags, stream, cq);
 }
 
 // ---- batch-invariant projection GEMM
@@ -914,6 +922,42 @@ csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32
   cudaError_t e = csa::launch_gemm_fp8(w_packed, n_out, k_in, groups, x, n_tok, out, workspace, sms,
                                        (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "fp8 gemm launch");
+  return CSA_OK;
+}
+
+csa_status csa_head_norm(int64_t n_tok, int32_t dim, int32_t rope, double eps, const int64_t* positions,
+                         const double* theta, const csa_head_norm_part* q, const csa_head_norm_part* k,
+                         csa_stream_t stream) {
+  if (dim < 2 || dim > csa::head_norm_max_dim() || dim % 2) return fail(CSA_ERR_ARG, "dim must be even, in [2, 1024]");
+  if (rope < 0 || rope > dim || rope % 2) return fail(CSA_ERR_ARG, "rope must be even, in [0, dim]");
+  if (!(eps >= 0.0 && eps <= 1e30)) return fail(CSA_ERR_ARG, "eps must be in [0, 1e30]");
+  if (n_tok < 0 || n_tok > 0x7FFFFFFF) return fail(CSA_ERR_ARG, "n_tok must be in [0, 2^31)");
+  if (!q && !k) return fail(CSA_ERR_ARG, "NULL argument");
+  csa::HeadNormArgs a{};
+  a.n_tok = n_tok; a.positions = positions; a.theta = theta; a.eps = eps; a.dim = dim; a.rope = rope;
+  int64_t heads = 0;
+  const csa_head_norm_part* part[2] = {q, k};
+  for (int s = 0; s < 2; ++s) {
+    const csa_head_norm_part* p = part[s];
+    if (!p) continue;
+    if (p->heads < 0 || p->heads > 65536) return fail(CSA_ERR_ARG, "heads must be in [0, 65536]");
+    if (p->heads == 0 || n_tok == 0) continue;
+    if (!p->x || !p->y) return fail(CSA_ERR_ARG, "NULL argument");
+    const uintptr_t el = p->f32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(p->x) % el || reinterpret_cast<uintptr_t>(p->y) % el ||
+        reinterpret_cast<uintptr_t>(p->weight) % 4)
+      return fail(CSA_ERR_ARG, "x, y or weight is not aligned to its elements");
+    const bool rotate = p->rotate && rope > 0;
+    if (rotate && (!positions || !theta)) return fail(CSA_ERR_ARG, "rotated heads need positions and theta");
+    a.part[s] = csa::HeadNormPart{p->x, p->y, p->weight, p->x_token_stride, p->x_head_stride, p->y_token_stride,
+                                  p->y_head_stride, p->heads, p->f32 ? 1 : 0, rotate ? 1 : 0, 0, 0, 0};
+    heads += p->heads;
+  }
+  if (heads == 0) return CSA_OK;
+  const int sms = sm_count();
+  if (sms <= 0) return fail(CSA_ERR_CUDA, "cannot query the SM count");
+  cudaError_t e = csa::launch_head_norm(a, sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "head norm launch");
   return CSA_OK;
 }
 

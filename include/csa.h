@@ -95,6 +95,14 @@ typedef enum {
  */
 #define CSA_ATTN_STATE_READY 0x100
 
+/*
+ * Flag OR-ed into the variant of csa_hca_decode_attn and csa_prefill_chunk:
+ * the last D_rope dims of q are rotated already (csa_head_norm), and the
+ * attention takes q as it is.  Without it the attention rotates them at the
+ * query's position.
+ */
+#define CSA_ATTN_Q_ROTATED 0x200
+
 /* Storage format of a cache (csa_cfg.fmt). */
 typedef enum {
   CSA_FMT_MIXED = 0,            /* the pages' formats: KV rows FP8 E4M3 (non-RoPE
@@ -325,8 +333,9 @@ csa_status csa_index_topk(const csa_cache_t* cache, int32_t layer, int32_t n,
  *                         CSA_ERR_ARG (whichever fold runs).
  *   CSA_VARIANT_AUTO      LOW_OCC when the workspace suffices and HIGH_OCC
  *                         would leave SMs idle, else HIGH_OCC.
- * All three return identical bits.  Any of them may carry the flag
- * CSA_ATTN_STATE_READY (defined with csa_variant above).  The workspace is
+ * All three return identical bits.  Any of them may carry the flags
+ * CSA_ATTN_STATE_READY and CSA_ATTN_Q_ROTATED (defined with csa_variant
+ * above).  The workspace is
  * scratch owned by the caller; its contents before and after the call are
  * irrelevant, and it must not be used by other work on the stream until the
  * call's kernels finish.
@@ -451,8 +460,9 @@ csa_status csa_decode_step(csa_cache_t* cache, int32_t layer, int32_t n, const i
  *              copies, per-query request ids, scores [n n_tok][ld] with
  *              ld = max(128 x max_pages_per_request, 128), counts, indices,
  *              the split attention's partials when the variant takes it)
- *   variant    AUTO / HIGH_OCC / LOW_OCC, as the three calls (no flags);
- *              every variant returns identical bits
+ *   variant    AUTO / HIGH_OCC / LOW_OCC, as the three calls, with
+ *              CSA_ATTN_Q_ROTATED when q is rotated already (no other
+ *              flag); every variant returns identical bits
  * Limits: n * n_tok <= 65535.  Errors: CSA_ERR_ARG for a bad shape, a NULL
  * or a short or misaligned workspace (nothing launched); otherwise as the
  * calls it makes.  Asynchronous.
@@ -579,6 +589,50 @@ size_t     csa_gemm_fp8_workspace_bytes(int32_t n_out, int32_t k_in, int32_t gro
 csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32_t groups, const uint16_t* x,
                         int32_t n_tok, int32_t n_seg, const csa_gemm_out* segs, void* workspace,
                         size_t workspace_bytes, csa_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * RMS norm of every query head and key head and the partial RoPE, in one
+ * launch between the projections and the attention:
+ *   y = w * x / sqrt(mean(x^2) + eps)   over the head's `dim` values, then
+ *   the pairs (2i, 2i+1) of the last `rope` dims rotated by the angle
+ *   position * theta[i].
+ * The queries are rotated at the token's position (the attention then takes
+ * CSA_ATTN_Q_ROTATED); the compressor's KV candidates are normed only (the
+ * append rotates their pooled entries), keys of their own attention both.
+ *
+ * fp32 arithmetic with fp64 angles, one rounding to the output's type.  A
+ * head with an infinity or a NaN comes out as the formula gives it, and no
+ * other head does; a head of zeros with eps = 0 is NaN.
+ *
+ *   n_tok      0 .. 2^31 - 1 (heads x tokens so that the launch has at most
+ *              2^31 - 1 blocks; a block takes at least 4 heads)
+ *   dim        even, 2 .. 1024;  rope even, 0 .. dim;  eps in [0, 1e30]
+ *   positions  device int64 [n_tok], theta device fp64 [rope / 2]; may be
+ *              NULL when nothing is rotated
+ *   q, k       host descriptors, read during the call; NULL or heads = 0:
+ *              none.  x and y: device, element (token t, head h, dim d) at
+ *              t * token_stride + h * head_stride + d (strides in elements;
+ *              dims contiguous), fp32 when `f32`, else BF16, aligned to
+ *              their elements (on 16 bytes with dim a multiple of 8 the
+ *              loads are 16 bytes wide).  y may be x with its strides (in
+ *              place); otherwise no output may overlap an input.  weight:
+ *              device fp32 [dim], or NULL for ones.  rotate: whether the
+ *              last dims are rotated.
+ * Asynchronous.
+ * ------------------------------------------------------------------- */
+typedef struct {
+  const void* x;
+  void* y;
+  const float* weight;
+  int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+  int32_t heads;                /* 0 .. 65536 */
+  int32_t f32;
+  int32_t rotate;
+} csa_head_norm_part;
+
+csa_status csa_head_norm(int64_t n_tok, int32_t dim, int32_t rope, double eps, const int64_t* positions,
+                         const double* theta, const csa_head_norm_part* q, const csa_head_norm_part* k,
+                         csa_stream_t stream);
 
 /*
  * Read and clear the device error word (synchronises `stream`).  Returns

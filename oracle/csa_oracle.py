@@ -437,6 +437,18 @@ def fp8_linear(x, codes, scales, groups: int = 1) -> np.ndarray:
     return grouped_linear(xd, wd, groups)
 
 
+def head_norm(x, weight, eps: float, pos=None, R: int = 0, base: float = 10000.0) -> np.ndarray:
+    """RMS norm over the last axis of heads x [n, heads, D], and RoPE on its
+    last R dims at the tokens' positions pos [n] when given."""
+    x = np.asarray(x, np.float64)
+    y = x / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + eps)
+    if weight is not None:
+        y = y * np.asarray(weight, np.float64)
+    if pos is None or R == 0:
+        return y
+    return rope(y, np.broadcast_to(np.asarray(pos)[:, None], y.shape[:2]), R, base)
+
+
 # ---------------------------------------------------------------------------
 # Lightning indexer.  [V4-来了] section "CSA——压缩稀疏注意力": the query's hidden
 # state is projected down and up to multi-head index queries, passed through

@@ -202,3 +202,38 @@ def test_fp8_gemm_shapes_and_argument_errors_on_the_host(cuda_lib):
     assert cuda_lib.csa_gemm_fp8_pack_weight(P, P, 256, 64, 1, P, 100, None) == -2
     assert cuda_lib.csa_gemm_fp8_workspace_bytes(256, 64, 1, 0) == 0
     assert cuda_lib.csa_gemm_fp8_workspace_bytes(256, 64, 1, (1 << 20) + 1) == 0
+
+
+def test_head_norm_argument_errors_on_the_host(cuda_lib):
+    """csa_head_norm refuses bad arguments before any launch (the pointers
+    below are never touched)."""
+    P = 0x10000
+    f = cuda_lib.csa_head_norm
+
+    def part(**kw):
+        d = dict(x=P, y=P, weight=P, x_token_stride=512, x_head_stride=64, y_token_stride=512, y_head_stride=64, heads=8,
+                 f32=1, rotate=1)
+        d.update(kw)
+        return ctypes.cast(ctypes.pointer(_lib.HeadNormPart(*[d[n] for n, _ in _lib.HeadNormPart._fields_])), ctypes.c_void_p)
+
+    q = part()
+    nan = float("nan")
+    cases = [
+        ((4, 63, 16, 1e-6, P, P, q, None, None), b"dim"), ((4, 1026, 16, 1e-6, P, P, q, None, None), b"dim"),
+        ((4, 64, 66, 1e-6, P, P, q, None, None), b"rope"), ((4, 64, 3, 1e-6, P, P, q, None, None), b"rope"),
+        ((4, 64, 16, -1.0, P, P, q, None, None), b"eps"), ((4, 64, 16, nan, P, P, q, None, None), b"eps"),
+        ((-1, 64, 16, 1e-6, P, P, q, None, None), b"n_tok"), ((1 << 31, 64, 16, 1e-6, P, P, q, None, None), b"n_tok"),
+        ((4, 64, 16, 1e-6, P, P, None, None, None), b"NULL"), ((4, 64, 16, 1e-6, None, P, q, None, None), b"positions"),
+        ((4, 64, 16, 1e-6, P, None, q, None, None), b"positions"),
+        ((4, 64, 16, 1e-6, P, P, part(x=None), None, None), b"NULL"), ((4, 64, 16, 1e-6, P, P, q, part(y=None), None), b"NULL"),
+        ((4, 64, 16, 1e-6, P, P, part(x=P + 2), None, None), b"aligned"),
+        ((4, 64, 16, 1e-6, P, P, part(weight=P + 2), None, None), b"aligned"),
+        ((4, 64, 16, 1e-6, P, P, part(f32=0, y=P + 1), None, None), b"aligned"),
+        ((4, 64, 16, 1e-6, P, P, part(heads=-1), None, None), b"heads"),
+        ((4, 64, 16, 1e-6, P, P, q, part(heads=65537), None), b"heads"),
+    ]
+    for args, msg in cases:
+        assert f(*args) == -1, args
+        assert msg in cuda_lib.csa_last_error(), (args, cuda_lib.csa_last_error())
+    assert f(0, 64, 16, 1e-6, None, None, q, None, None) == 0              # no tokens: nothing to do
+    assert f(4, 64, 16, 1e-6, None, None, part(heads=0), None, None) == 0  # no heads
