@@ -728,8 +728,9 @@ class LinearFP8:
     def __call__(self, x: torch.Tensor, outs, workspace: torch.Tensor | None = None, stream=None):
         """x: CUDA BF16 [n_tok][k_in].  outs: one tensor or a list of CUDA
         tensors [n_tok][rows_s] (BF16 or fp32, contiguous) whose rows add up
-        to n_out, as Linear's.  Unless `workspace` is given, the call takes
-        scratch of its own from the allocator.  Returns outs."""
+        to n_out, as Linear's.  A call of more than 64 tokens needs scratch:
+        unless `workspace` is given, it takes its own from the allocator.
+        Returns outs."""
         segs = [outs] if isinstance(outs, torch.Tensor) else outs
         n = x.shape[0] if x.dim() == 2 else -1
         _need(x, torch.bfloat16, (n, self.k_in), "x")
@@ -745,17 +746,20 @@ class LinearFP8:
         if n == 0:
             return outs
         with _current_device(self.device):
-            if workspace is None:
-                workspace = _scratch(self.workspace_bytes(n) + 256, self.device, stream)
-            else:
+            need = self.workspace_bytes(n)
+            if workspace is not None:
                 _need(workspace, torch.uint8, name="workspace")
                 if workspace.device != self.device:
                     raise ValueError("workspace must be on the weight's device")
-            at = workspace.data_ptr()
-            ws = (at + 255) // 256 * 256
+            elif need:
+                workspace = _scratch(need + 256, self.device, stream)
+            at = ws = size = 0
+            if workspace is not None:
+                at = workspace.data_ptr()
+                ws = (at + 255) // 256 * 256
+                size = workspace.numel() - (ws - at)
             check(self.lib.csa_gemm_fp8(self.packed.data_ptr(), self.n_out, self.k_in, self.groups, x.data_ptr(), n,
-                                        len(segs), arr, ws, workspace.numel() - (ws - at), _stream(stream)),
-                  "csa_gemm_fp8")
+                                        len(segs), arr, ws, size, _stream(stream)), "csa_gemm_fp8")
         return outs
 
     @staticmethod

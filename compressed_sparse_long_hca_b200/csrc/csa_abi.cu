@@ -911,13 +911,14 @@ csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32
     if (reinterpret_cast<uintptr_t>(segs[s].y) % (segs[s].bf16 ? 2 : 4))
       return fail(CSA_ERR_ARG, "an output segment is not aligned to its elements");
   if (n_tok == 0) return CSA_OK;
-  if (!w_packed || !x || !workspace) return fail(CSA_ERR_ARG, "NULL argument");
+  if (!w_packed || !x) return fail(CSA_ERR_ARG, "NULL argument");
   if (reinterpret_cast<uintptr_t>(x) % 2) return fail(CSA_ERR_ARG, "x must be 2-byte aligned");
   if (reinterpret_cast<uintptr_t>(w_packed) % 16 || reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(CSA_ERR_ARG, "w_packed must be 16-byte and workspace 256-byte aligned");
   const int sms = sm_count();
   if (sms <= 0) return fail(CSA_ERR_CUDA, "cannot query the SM count");
-  if (workspace_bytes < csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok, sms))
+  const size_t need = csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok, sms);
+  if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(CSA_ERR_ARG, "workspace smaller than csa_gemm_fp8_workspace_bytes");
   cudaError_t e = csa::launch_gemm_fp8(w_packed, n_out, k_in, groups, x, n_tok, out, workspace, sms,
                                        (cudaStream_t)stream);

@@ -19,17 +19,27 @@
 // Scales travel in 512-byte chunks (128 rows x 4 blocks) with every fourth
 // block and are copied to TMEM in front of the MMAs that read them.
 //
-// Batch invariance.  A weight with few row tiles cuts K into S parts, S from
-// the weight's shape and the SM count alone; the parts are summed in fp32 in
-// part order.  Two forms of the launch add the same numbers in the same order:
-//   spread  (few tokens): one work item per (row tile, token tile, part); each
-//           writes its fp32 partial, the item that finishes a tile last adds
-//           the parts in order;
-//   whole   (many tokens): one work item per (row tile, token tile), its parts
-//           one after the other into alternating TMEM accumulators, summed in
-//           the epilogue's registers.
+// Batch invariance.  A weight with few row tiles cuts K into S parts (at most
+// 8), S from the weight's shape and the SM count alone; the parts are summed
+// in fp32 in part order.  The forms of the launch add the same numbers in the
+// same order:
+//   spread  one thread-block cluster per (row tile, token tile), a CTA per
+//           part; the CTAs leave their fp32 partials in their own shared
+//           memory and each adds the parts of its share of the tokens through
+//           distributed shared memory;
+//   whole   one work item per (row tile, token tile) of a persistent CTA, its
+//           parts one after the other into alternating TMEM accumulators,
+//           summed in the epilogue's registers.
 // The K order inside a part is fixed and a token's column does not enter the
 // arithmetic of the others, so a token's bits depend on its row and the weight.
+//
+// Up to 64 tokens (a weight stream) the call is one launch without scratch:
+// four warps of each CTA quantise the tokens' block of every stage from global
+// memory straight into the MMA's operand layout, a few blocks ahead.  Beyond
+// that the quantised tokens are worth keeping: a kernel packs them once, and
+// the product's CTAs read blocks of them by bulk copies.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -37,6 +47,8 @@
 #include "tc.cuh"
 
 namespace csa {
+
+namespace cg = cooperative_groups;
 
 // Device error word of this product: first error wins.
 __device__ int32_t g_fp8_err[2];
@@ -49,41 +61,49 @@ constexpr int kWTileBytes = kRowTile * kKBlk; // 16 KB
 constexpr int kSfBytes = 512;                 // scales of 128 rows x 4 blocks, tcgen05.cp order
 constexpr int kSfRing = 4;                    // scale buffers in TMEM
 constexpr int kMinPartBlocks = 4;             // K blocks of the smallest part
+constexpr int kMaxParts = 8;                  // parts of a weight: CTAs of the largest portable cluster
+constexpr int kFuseTokens = 64;               // most tokens that the product quantises itself
 
 struct Fp8Args {
   const uint8_t* w;       // packed weight: tiles [row_tiles][k_blocks][16 KB]
   const uint8_t* wsf;     // its scales: chunks [row_tiles][sup][512]
   const uint8_t* xp;      // packed activations [groups][k_blocks][tok_tiles][tile_n * 128]
   const uint8_t* xsf;     // their scales: chunks [groups][sup][tok_tiles][chunks][512]
+  const uint16_t* x;      // fused quantisation: the BF16 tokens [n_tok][groups * kg]
+  int x_aligned;          // x on 16 bytes (every block's row then is: kg is a multiple of 8)
+  int kg;
   int n_out, n_tok;
   int row_tiles, k_blocks, sup;   // sup: scale chunks along K, ceil(k_blocks / 4)
   int groups, splits;
-  int tok_tiles, tile_n;          // token tiles of tile_n tokens (a multiple of 32)
+  int tok_tiles, tile_n;          // token tiles of tile_n tokens (a multiple of 16)
   int spread;
-  int items;
+  int tiles;                      // row_tiles * tok_tiles
   GemmOut out;
-  float* part;            // spread, splits > 1: [splits][n_tok][n_out] fp32 partials
-  int32_t* done;          // spread, splits > 1: [row_tiles][tok_tiles] parts finished
 };
 
-// NT: most tokens of a tile.
-template <int NT>
+// NT: most tokens of a tile.  FUSE: the tokens are quantised by this kernel.
+template <int NT, bool FUSE>
 struct Cfg {
   static constexpr int kSets = NT >= 128 ? 2 : 1;          // sets of 4 epilogue warps, each a share of the columns
   static constexpr int kCols = NT / kSets;                 // accumulator columns of a set
-  static constexpr int kThreads = 64 + 128 * kSets;
+  static constexpr int kEpi = 128 * kSets;
+  static constexpr int kThreads = 64 + kEpi + (FUSE ? 128 : 0);
   static constexpr int kPerSm = NT <= 64 ? 2 : 1;          // CTAs per SM
   static constexpr int kChunks = (NT + 127) / 128;         // scale chunks of a token tile
   static constexpr int kStageBytes = kWTileBytes + NT * kKBlk + kSfBytes * (1 + kChunks);
   static constexpr int kStagesFit = (kPerSm == 2 ? 110 : 224) * 1024 / kStageBytes;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
-  static constexpr uint32_t kSfCols = 4 * (1 + kChunks);   // TMEM columns of one scale buffer
-  static constexpr uint32_t kSfBase = 2 * NT;
-  static constexpr uint32_t kColsNeeded = 2 * NT + kSfRing * kSfCols;
+  static constexpr int kUnits = NT / 16;                   // fused: 16-value units of a thread per block
+  static constexpr int kAhead = NT <= 16 ? 6 : NT <= 32 ? 3 : NT <= 48 ? 2 : 1;   // blocks it loads ahead (48 registers)
+  // TMEM: two accumulators, the weight's scale ring, the tokens' scale ring
+  static constexpr uint32_t kXsfRing = FUSE ? 8 : kSfRing;
+  static constexpr uint32_t kWsfBase = 2 * NT, kXsfBase = kWsfBase + 4 * kSfRing;
+  static constexpr uint32_t kColsNeeded = kXsfBase + 4 * kChunks * kXsfRing;
   static constexpr uint32_t kTmemCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
   static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 256 + 128;
   static_assert(kColsNeeded <= 512 && kTmemCols * kPerSm <= 512, "TMEM");
   static_assert(kStages >= 3 && kStages <= 8, "stages");
+  static_assert(kRowTile * NT * 4 <= kStages * kStageBytes, "a part's sums fit in the ring");
 };
 
 // The first K block of part p (parts differ by at most one block).
@@ -91,97 +111,149 @@ __host__ __device__ inline int part_begin(int k_blocks, int splits, int p) {
   return (int)((int64_t)k_blocks * p / splits);
 }
 
-__device__ __forceinline__ void g_store(void* base, int64_t at, bool bf16, float v) {
-  if (bf16) static_cast<uint16_t*>(base)[at] = bf16_rn(v);
-  else static_cast<float*>(base)[at] = v;
+// Where an output feature goes: element (token t) at y + t * rows.
+struct OutRow {
+  void* y;
+  int64_t rows;
+  bool bf16;
+  __device__ __forceinline__ void store(int t, float v) const {
+    if (bf16) static_cast<uint16_t*>(y)[t * rows] = bf16_rn(v);
+    else static_cast<float*>(y)[t * rows] = v;
+  }
+  // Tokens t .. t + 15, the first n of them.
+  __device__ __forceinline__ void store16(int t, int n, const float* v) const {
+    if (bf16) {
+      uint16_t* p = static_cast<uint16_t*>(y) + t * rows;
+#pragma unroll
+      for (int e = 0; e < 16; ++e, p += rows)
+        if (e < n) *p = bf16_rn(v[e]);
+    } else {
+      float* p = static_cast<float*>(y) + t * rows;
+#pragma unroll
+      for (int e = 0; e < 16; ++e, p += rows)
+        if (e < n) *p = v[e];
+    }
+  }
+};
+
+__device__ __forceinline__ OutRow out_row(const GemmOut& out, int o) {
+  int sg = 0;
+  while (sg + 1 < out.n_seg && o >= out.seg_end[sg]) ++sg;
+  const int r0 = sg > 0 ? out.seg_end[sg - 1] : 0;
+  const bool bf16 = (out.bf16_mask >> sg) & 1u;
+  char* y = static_cast<char*>(out.y[sg]);
+  return OutRow{y + (int64_t)(o - r0) * (bf16 ? 2 : 4), out.seg_end[sg] - r0, bf16};
 }
 
 }  // namespace
 
-// The least e with amax <= 448 * 2^e, clamped to E8M0's range; 0 for an empty
-// block.  448 = 1.75 * 2^8, so e follows from amax's exponent and mantissa.
-__device__ __forceinline__ int fp8_exponent(float amax) {
-  if (!(amax > 0.f)) return 0;
-  int e = ilogbf(amax);
-  const float m = scale_pow2(amax, e);               // [1, 2)
-  e = e - 8 + (m > 1.75f ? 1 : 0);
-  return e < -127 ? -127 : (e > 127 ? 127 : e);
+// The least e >= -127 with amax <= 448 * 2^e of the BF16 magnitude with bits
+// `top` (finite); 0 for an empty block.  448 = 1.75 * 2^8, so e follows from
+// the exponent field and whether the mantissa exceeds 1.75; subnormals and
+// what else is below 2^-127 * 448 end at -127.
+__device__ __forceinline__ int fp8_exponent(uint32_t top) {
+  const int e = (int)(top >> 7) - 135 + ((top & 0x7Fu) > 96u ? 1 : 0);
+  return top == 0 ? 0 : (e < -127 ? -127 : e);
 }
 
-// Quantise X (BF16 [n_tok][groups * kg]) into the B operand's blocks: a thread
-// takes 16 values, the 8 threads of a (token, block) share its scale.  A block
-// that holds an infinity or a NaN gets the NaN scale: every output of that
-// token is then NaN.  Rows beyond n_tok of the last tile and columns beyond kg
+// 16 BF16 values of one row's block as loaded (columns beyond kg are zero).
+struct Unit {
+  uint32_t w[8];
+};
+
+__device__ __forceinline__ Unit load_unit(const uint16_t* p, int cols, bool aligned) {
+  Unit u;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {                          // kg is a multiple of 8: a half is whole or absent
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (8 * h < cols) {
+      if (aligned) {
+        v = *reinterpret_cast<const uint4*>(p + 8 * h);
+      } else {
+        const uint16_t* s = p + 8 * h;
+        v.x = (uint32_t)s[0] | ((uint32_t)s[1] << 16);
+        v.y = (uint32_t)s[2] | ((uint32_t)s[3] << 16);
+        v.z = (uint32_t)s[4] | ((uint32_t)s[5] << 16);
+        v.w = (uint32_t)s[6] | ((uint32_t)s[7] << 16);
+      }
+    }
+    u.w[4 * h] = v.x; u.w[4 * h + 1] = v.y; u.w[4 * h + 2] = v.z; u.w[4 * h + 3] = v.w;
+  }
+  return u;
+}
+
+// Quantise a unit; the 8 lanes that differ in lane bits 2-4 hold one block of
+// a row and share its scale.  `codes`: the 16 E4M3 codes.  Returns the scale
+// byte: 255 (NaN, codes 0) for a block that holds an infinity or a NaN.
+__device__ __forceinline__ uint32_t quant_unit(const Unit& u, uint4& codes) {
+  // the largest magnitude: BF16 bits without the sign order as integers
+  // (infinity 0x7F80, NaN above it)
+  uint32_t top = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) top = __vmaxu2(top, u.w[q] & 0x7FFF7FFFu);
+  top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool finite = top < 0x7F80u;
+  const int e = finite ? fp8_exponent(top) : 0;
+  const float inv = exp2i(-e);                           // -e in [-120, 127]: a normal fp32, the product exact or below half a code
+  uint32_t pk[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t v = u.w[2 * q + h];
+      const float2 f = make_float2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xFFFF0000u) * inv);
+      r |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << (16 * h);
+    }
+    pk[q] = finite ? r : 0u;
+  }
+  codes = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  return (uint32_t)(finite ? e + 127 : 255);
+}
+
+// Offset of row r's 16-byte column c in a block of rows x 128 codes (no-swizzle
+// K-major core matrices), and of row r's scale word in a 512-byte chunk.
+__device__ __forceinline__ int code_off(int r, int c) { return (r >> 3) * 1024 + c * 128 + (r & 7) * 16; }
+__device__ __forceinline__ int scale_off(int r) { return 16 * (r & 31) + 4 * ((r >> 5) & 3); }
+
+// Quantise X (BF16 [n_tok][groups * kg]) into the B operand's blocks, 16
+// values a thread.  Rows beyond n_tok of the last tile and columns beyond kg
 // of the last block are zero; scales nothing reads are left as they are.
-// Also clears the row tiles' part counters.
 __global__ void __launch_bounds__(256) fp8_quant_x_kernel(const uint16_t* x, int n_tok, int kg, int64_t row_len,
                                                           int k_blocks, int sup, int tok_tiles, int tile_n, int chunks,
-                                                          bool aligned, uint8_t* xp, uint8_t* xsf, int32_t* done,
-                                                          int n_done) {
+                                                          bool aligned, uint8_t* xp, uint8_t* xsf) {
   tc::griddep_launch_dependents();
-  if (done != nullptr && blockIdx.x == 0 && blockIdx.y == 0)
-    for (int u = threadIdx.x; u < n_done; u += blockDim.x) done[u] = 0;
+  tc::griddep_wait();
   const int g = blockIdx.y;
   x += (int64_t)g * kg;
   xp += (int64_t)g * k_blocks * tok_tiles * tile_n * kKBlk;
   xsf += (int64_t)g * sup * tok_tiles * chunks * kSfBytes;
-  const int n_pad = tok_tiles * tile_n;
+  const int n_pad = tok_tiles * tile_n;                  // a multiple of 4
   const int64_t total = (int64_t)k_blocks * n_pad * 8;
   for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < total; u += (int64_t)gridDim.x * blockDim.x) {
-    const int c = (int)(u & 7);
-    const int t = (int)((u >> 3) % n_pad);
-    const int b = (int)((u >> 3) / n_pad);
+    // 32 consecutive units: 4 rows, the row in lane bits 0-1, the column in bits 2-4
+    const int c = (int)((u >> 2) & 7);
+    const int64_t row = (u >> 5) * 4 + (u & 3);
+    const int t = (int)(row % n_pad), b = (int)(row / n_pad);
     const int k0 = b * kKBlk + c * 16;
-    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (t < n_tok) {
-      const uint16_t* p = x + (int64_t)t * row_len + k0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {                  // kg is a multiple of 8: a half is whole or absent
-        if (k0 + 8 * h >= kg) break;
-        if (aligned) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p + 8 * h);
-          w[4 * h] = v.x; w[4 * h + 1] = v.y; w[4 * h + 2] = v.z; w[4 * h + 3] = v.w;
-        } else {
-          for (int q = 0; q < 4; ++q) w[4 * h + q] = (uint32_t)p[8 * h + 2 * q] | ((uint32_t)p[8 * h + 2 * q + 1] << 16);
-        }
-      }
-    }
-    // the largest magnitude: BF16 bits without the sign order as integers
-    // (infinity 0x7F80, NaN above it)
-    uint32_t top = 0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) top = __vmaxu2(top, w[q] & 0x7FFF7FFFu);
-    top = max(top & 0xFFFFu, top >> 16);
-    for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool finite = top < 0x7F80u;
-    const int e = finite ? fp8_exponent(bf16_val((uint16_t)top)) : 0;
-    uint32_t pk[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t r = 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t v = w[2 * q + h];
-        const float lo = scale_pow2(bf16_val((uint16_t)(v & 0xFFFFu)), e), hi = scale_pow2(bf16_val((uint16_t)(v >> 16)), e);
-        r |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3) << (16 * h);
-      }
-      pk[q] = finite ? r : 0u;
-    }
+    const Unit v = load_unit(x + (int64_t)t * row_len + k0, t < n_tok ? kg - k0 : 0, aligned);
+    uint4 codes;
+    const uint32_t sf = quant_unit(v, codes);
     const int j = t / tile_n, r = t % tile_n;
-    uint8_t* dst = xp + ((int64_t)b * tok_tiles + j) * tile_n * kKBlk + (r >> 3) * 1024 + c * 128 + (r & 7) * 16;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    if (c == 0)
-      xsf[(((int64_t)(b >> 2) * tok_tiles + j) * chunks + (r >> 7)) * kSfBytes + 16 * (r & 31) + 4 * ((r >> 5) & 3) + (b & 3)] =
-          (uint8_t)(finite ? e + 127 : 255);
+    *reinterpret_cast<uint4*>(xp + ((int64_t)b * tok_tiles + j) * tile_n * kKBlk + code_off(r, c)) = codes;
+    if (c == 0) xsf[(((int64_t)(b >> 2) * tok_tiles + j) * chunks + (r >> 7)) * kSfBytes + scale_off(r) + (b & 3)] = (uint8_t)sf;
   }
 }
 
-// Persistent CTAs over the work items.  Warp 0 issues the bulk copies, warp 1
-// the scale copies and MMAs (one elected lane each), the others read the
-// accumulators (a thread = one output feature, its columns = tokens).
-template <int NT>
-__global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kPerSm) fp8_gemm_kernel(Fp8Args a) {
-  using C = Cfg<NT>;
+// Warp 0 issues the bulk copies, warp 1 the scale copies and MMAs (one elected
+// lane each), the next 4 or 8 read the accumulators (a thread = one output
+// feature, its columns = tokens), the last 4 (FUSE) quantise the tokens.
+template <int NT, bool FUSE>
+__global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm)
+    fp8_gemm_kernel(const __grid_constant__ Fp8Args a) {
+  using C = Cfg<NT, FUSE>;
   constexpr int S = C::kStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -192,17 +264,18 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kPerSm) fp8_gemm_k
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* last_flag = abort_flag + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr uint64_t kLimit = 1000000000ull;
+  constexpr int kXOff = kWTileBytes, kWsfOff = kXOff + NT * kKBlk, kXsfOff = kWsfOff + kSfBytes;   // in a stage
 
+  tc::griddep_launch_dependents();
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, C::kTmemCols);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) { tc::mbar_init(&full[s], 1); tc::mbar_init(&empty[s], 1); }
-    for (int x = 0; x < 2; ++x) { tc::mbar_init(&acc_full[x], 1); tc::mbar_init(&acc_empty[x], 128 * C::kSets); }
+    for (int s = 0; s < S; ++s) { tc::mbar_init(&full[s], FUSE ? 5 : 1); tc::mbar_init(&empty[s], 1); }
+    for (int x = 0; x < 2; ++x) { tc::mbar_init(&acc_full[x], 1); tc::mbar_init(&acc_empty[x], C::kEpi); }
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -214,58 +287,46 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kPerSm) fp8_gemm_k
   const int rows_per_group = a.n_out / a.groups;
   const int xb = a.tile_n * kKBlk;                      // bytes of one packed activation block
   const int n_sfb = (a.tile_n + 127) / 128;             // its scale chunks
-  const uint32_t sf_bytes = (uint32_t)(kSfBytes * (1 + n_sfb));
-  const int n_parts = a.spread ? a.splits : 1;          // work items per tile
 
-  // work item -> row tile, token tile, K blocks [k0, k1)
-  auto item_tile = [&](int it, int& rt, int& tt, int& p) {
-    p = it % n_parts;
-    it /= n_parts;
-    tt = it % a.tok_tiles;
-    rt = it / a.tok_tiles;
-  };
-  auto item_k = [&](int p, int& k0, int& k1) {
-    k0 = a.spread ? part_begin(a.k_blocks, a.splits, p) : 0;
-    k1 = a.spread ? part_begin(a.k_blocks, a.splits, p + 1) : a.k_blocks;
-  };
+  // Spread: this CTA's part of one tile.  Whole: every part of the tiles
+  // blockIdx.x, blockIdx.x + gridDim.x, ...
+  const int part = a.spread ? (int)(blockIdx.x % a.splits) : 0;
+  const int it0 = a.spread ? (int)(blockIdx.x / a.splits) : (int)blockIdx.x;
+  const int it_step = a.spread ? a.tiles : (int)gridDim.x;
+  const int k0 = a.spread ? part_begin(a.k_blocks, a.splits, part) : 0;
+  const int k1 = a.spread ? part_begin(a.k_blocks, a.splits, part + 1) : a.k_blocks;
+  const int q0 = part, q1 = a.spread ? part + 1 : a.splits;
   bool ok = true;
   uint32_t issued = 0;                                  // producer: stages filled
   if (warp == 0) {
-    // ---- producer.  The weight does not depend on the quantising kernel
-    //      ahead: the first stages' weight copies are issued before waiting
-    //      for it.
-    bool waited = false;
+    // ---- producer.  The weight does not depend on the kernels ahead (the
+    //      packing ends with a kernel of its own): its first stages are
+    //      issued before waiting for them.
+    bool waited = FUSE;
     uint32_t pre = 0;                                   // stages whose weight copies are already issued
     auto put_w = [&](uint32_t x, int rt, int kb, bool sf) {
       uint8_t* st = sm + (size_t)(x % S) * C::kStageBytes;
-      tc::mbar_arrive_expect_tx(&full[x % S], (uint32_t)(kWTileBytes + xb) + (sf ? sf_bytes : 0u));
+      const uint32_t xbytes = FUSE ? 0u : (uint32_t)(xb + (sf ? kSfBytes * n_sfb : 0));
+      tc::mbar_arrive_expect_tx(&full[x % S], (uint32_t)(kWTileBytes + (sf ? kSfBytes : 0)) + xbytes);
       tc::bulk_g2s(st, a.w + ((int64_t)rt * a.k_blocks + kb) * kWTileBytes, kWTileBytes, &full[x % S]);
-      if (sf)
-        tc::bulk_g2s(st + kWTileBytes + NT * kKBlk, a.wsf + ((int64_t)rt * a.sup + (kb >> 2)) * kSfBytes, kSfBytes,
-                     &full[x % S]);
+      if (sf) tc::bulk_g2s(st + kWsfOff, a.wsf + ((int64_t)rt * a.sup + (kb >> 2)) * kSfBytes, kSfBytes, &full[x % S]);
     };
     auto put_x = [&](uint32_t x, int rt, int tt, int kb, bool sf) {
       uint8_t* st = sm + (size_t)(x % S) * C::kStageBytes;
       const int64_t grp = (rt * kRowTile) / rows_per_group;
-      tc::bulk_g2s(st + kWTileBytes, a.xp + ((grp * a.k_blocks + kb) * a.tok_tiles + tt) * xb, (uint32_t)xb, &full[x % S]);
+      tc::bulk_g2s(st + kXOff, a.xp + ((grp * a.k_blocks + kb) * a.tok_tiles + tt) * xb, (uint32_t)xb, &full[x % S]);
       if (sf)
-        tc::bulk_g2s(st + kWTileBytes + NT * kKBlk + kSfBytes,
-                     a.xsf + ((grp * a.sup + (kb >> 2)) * a.tok_tiles + tt) * n_sfb * kSfBytes,
+        tc::bulk_g2s(st + kXsfOff, a.xsf + ((grp * a.sup + (kb >> 2)) * a.tok_tiles + tt) * n_sfb * kSfBytes,
                      (uint32_t)(kSfBytes * n_sfb), &full[x % S]);
     };
-    {
-      int rt, tt, p, k0, k1;
-      item_tile(blockIdx.x, rt, tt, p);
-      item_k(p, k0, k1);
+    if (!FUSE) {
       pre = (uint32_t)(k1 - k0 < S ? k1 - k0 : S);
       if (tc::elect_one())
-        for (uint32_t x = 0; x < pre; ++x) put_w(x, rt, k0 + (int)x, x == 0 || ((k0 + (int)x) & 3) == 0);
+        for (uint32_t x = 0; x < pre; ++x) put_w(x, it0 / a.tok_tiles, k0 + (int)x, x == 0 || ((k0 + (int)x) & 3) == 0);
       __syncwarp();
     }
-    for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
-      int rt, tt, p, k0, k1;
-      item_tile(it, rt, tt, p);
-      item_k(p, k0, k1);
+    for (int it = it0; it < a.tiles && ok; it += it_step) {
+      const int rt = it / a.tok_tiles, tt = it % a.tok_tiles;
       if (!waited) { tc::griddep_wait(); waited = true; }
       for (int kb = k0; kb < k1; ++kb) {
         const uint32_t x = issued;
@@ -275,7 +336,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kPerSm) fp8_gemm_k
         const bool sf = kb == k0 || (kb & 3) == 0;
         if (tc::elect_one()) {
           if (x >= pre) put_w(x, rt, kb, sf);
-          put_x(x, rt, tt, kb, sf);
+          if (!FUSE) put_x(x, rt, tt, kb, sf);
         }
         __syncwarp();
         issued = x + 1;
@@ -290,11 +351,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kPerSm) fp8_gemm_k
   } else if (warp == 1) {
     // ---- scale copies and MMAs
     uint32_t x = 0, u = 0, nsf = 0;                     // stage, accumulator and scale-buffer counters
-    for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
-      int rt, tt, p, k0, k1;
-      item_tile(it, rt, tt, p);
-      item_k(p, k0, k1);
-      const int q0 = a.spread ? p : 0, q1 = a.spread ? p + 1 : a.splits;
+    for (int it = it0; it < a.tiles && ok; it += it_step) {
       for (int q = q0; q < q1 && ok; ++q, ++u) {
         const int b0 = part_begin(a.k_blocks, a.splits, q), b1 = part_begin(a.k_blocks, a.splits, q + 1);
         const uint32_t acc = tmem + (u & 1) * NT;
@@ -306,24 +363,25 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kPerSm) fp8_gemm_k
           tc::tc_fence_after();
           const bool sf = kb == k0 || (kb & 3) == 0;
           if (sf) ++nsf;
-          // A scale buffer is rewritten three loads after its own: by then the
-          // MMAs that read it are complete, for the stage just waited for was
-          // free (S <= 8 blocks back), or the accumulator two tiles back was.
-          const uint32_t sfc = tmem + C::kSfBase + ((nsf - 1) % kSfRing) * C::kSfCols;
-          const uint32_t wb = tc::smem_u32(sm + (size_t)(x % S) * C::kStageBytes), xbase = wb + kWTileBytes;
+          // A scale buffer of four blocks is rewritten four loads after its
+          // own: by then the MMAs that read it are complete, for the stage
+          // just waited for was free (S <= 8 blocks back), or the accumulator
+          // two tiles back was.  The tokens' buffers of one block (FUSE) are
+          // rewritten 8 >= S blocks later.
+          const uint32_t wsf = tmem + C::kWsfBase + ((nsf - 1) % kSfRing) * 4;
+          const uint32_t xsf = tmem + C::kXsfBase + (FUSE ? x % C::kXsfRing : (nsf - 1) % kSfRing) * 4 * C::kChunks;
+          const uint32_t wb = tc::smem_u32(sm + (size_t)(x % S) * C::kStageBytes), xbase = wb + kXOff;
           if (tc::elect_one()) {
-            if (sf) {
-              const uint32_t sb = wb + kWTileBytes + NT * kKBlk;
-              tc::tmem_cp_32x128b_x4(sfc, tc::smem_desc(sb, 128, 128));
+            if (sf) tc::tmem_cp_32x128b_x4(wsf, tc::smem_desc(wb + kWsfOff, 128, 128));
+            if (FUSE || sf)
               for (int ch = 0; ch < n_sfb; ++ch)
-                tc::tmem_cp_32x128b_x4(sfc + 4 + 4 * ch, tc::smem_desc(sb + kSfBytes * (1 + ch), 128, 128));
-            }
-            const uint32_t id = kb & 3;
-            const uint32_t idesc = tc::idesc_mxf8(kRowTile, a.tile_n, id, id);
+                tc::tmem_cp_32x128b_x4(xsf + 4 * ch, tc::smem_desc(wb + kXsfOff + kSfBytes * ch, 128, 128));
+            const uint32_t id = kb & 3, xid = FUSE ? 0u : id;
+            const uint32_t idesc = tc::idesc_mxf8(kRowTile, a.tile_n, id, xid);
 #pragma unroll
             for (int m = 0; m < 4; ++m)
               tc::mma_mxf8(acc, tc::smem_desc(wb + m * 256, 128, 1024), tc::smem_desc(xbase + m * 256, 128, 1024), idesc,
-                           sfc | (id << 30), (sfc + 4) | (id << 30), (kb > b0 || m > 0) ? 1u : 0u);
+                           wsf | (id << 30), xsf | (xid << 30), (kb > b0 || m > 0) ? 1u : 0u);
             tc::mma_commit(&empty[x % S]);
             if (kb == b1 - 1) tc::mma_commit(&acc_full[u & 1]);
           }
@@ -332,90 +390,155 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kPerSm) fp8_gemm_k
       }
     }
     if (!ok) *abort_flag = 1;
-  } else {
-    // ---- epilogue.  After an abort the warps still walk every item and reach
-    //      every named barrier (the work is skipped), so that none is left
-    //      waiting at a barrier another has left.
-    tc::griddep_wait();                                 // the part counters are cleared; outputs may be written
-    const int q4 = warp & 3, set = (warp - 2) >> 2;
-    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    const int c_lo = set * C::kCols;
-    const int et = tid - 64;
-    uint32_t u = 0;
-    for (int it = blockIdx.x; it < a.items; it += gridDim.x) {
-      int rt, tt, p;
-      item_tile(it, rt, tt, p);
-      const int q0 = a.spread ? p : 0, q1 = a.spread ? p + 1 : a.splits;
-      const int o = rt * kRowTile + q4 * 32 + lane;
-      const int t0 = tt * a.tile_n;
-      const int n_here = min(a.tile_n, a.n_tok - t0) - c_lo;      // this set's tokens (may be <= 0)
-      float acc[C::kCols];
-      for (int q = q0; q < q1; ++q, ++u) {
-        ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit) && !*abort_flag;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) continue;
-        tc::tc_fence_after();
+  } else if (FUSE && warp >= 2 + C::kEpi / 32) {
+    // ---- token quantiser: block after block of this CTA's tiles, the loads
+    //      kAhead blocks before their use
+    tc::griddep_wait();
+    const int qt = tid - 64 - C::kEpi;                  // unit: row (qt >> 5) * 4 + (qt & 3) + 16 i, column (qt >> 2) & 7
+    const int r0 = (qt >> 5) * 4 + (qt & 3), c = (qt >> 2) & 7;
+    const int n_units = a.tile_n / 16;
+    const int64_t row_len = (int64_t)a.groups * a.kg;
+    const int n_it = it0 < a.tiles ? (a.tiles - 1 - it0) / it_step + 1 : 0;
+    const int total = n_it * (k1 - k0);
+    int lit = it0, lkb = k0;                            // the next block to load
+    Unit v[C::kAhead][C::kUnits];
+    auto load = [&](Unit (&dst)[C::kUnits]) {
+      const int64_t grp = (lit * kRowTile) / rows_per_group;
+      const int col = lkb * kKBlk + c * 16;
+      const uint16_t* p = a.x + grp * a.kg + col;
 #pragma unroll
-        for (int c0 = 0; c0 < C::kCols; c0 += 16) {
-          if (c0 < n_here) {
-            uint32_t v[16];
-            tc::tmem_ld_x16(tmem + lane_base + (u & 1) * NT + c_lo + c0, v);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              acc[c0 + e] = q == q0 ? __uint_as_float(v[e]) : acc[c0 + e] + __uint_as_float(v[e]);
-          }
-        }
-        tc::tc_fence_before();
-        tc::mbar_arrive(&acc_empty[u & 1]);
+      for (int i = 0; i < C::kUnits; ++i) {
+        const int t = r0 + 16 * i;
+        const bool there = lit < a.tiles && i < n_units && t < a.n_tok;
+        dst[i] = load_unit(p + (int64_t)(there ? t : 0) * row_len, there ? a.kg - col : 0, a.x_aligned != 0);
       }
-      int sg = 0;
-      while (sg + 1 < a.out.n_seg && o >= a.out.seg_end[sg]) ++sg;
-      const int r0 = sg > 0 ? a.out.seg_end[sg - 1] : 0;
-      const int64_t rows = a.out.seg_end[sg] - r0;
-      const bool bf = (a.out.bf16_mask >> sg) & 1u;
-      void* y = a.out.y[sg];
-      const int64_t y0 = (int64_t)(t0 + c_lo) * rows + (o - r0);
-      const bool partial = a.spread && a.splits > 1;
-      if (ok && o < a.n_out) {
-        float* pw = partial ? a.part + ((int64_t)p * a.n_tok + t0 + c_lo) * a.n_out + o : nullptr;
+      if (++lkb == k1) { lkb = k0; lit += it_step; }
+    };
 #pragma unroll
-        for (int e = 0; e < C::kCols; ++e) {
-          if (e < n_here) {
-            if (partial) pw[(int64_t)e * a.n_out] = acc[e];
-            else g_store(y, y0 + (int64_t)e * rows, bf, acc[e]);
-          }
-        }
-      }
-      if (partial) {
-        // the item that finishes the tile last adds the parts in part order
-        __threadfence();
-        tc::named_bar_sync(1, 128 * C::kSets);
-        if (et == 0) last_flag[0] = atomicAdd(&a.done[rt * a.tok_tiles + tt], 1) == a.splits - 1 ? 1 : 0;
-        tc::named_bar_sync(1, 128 * C::kSets);
-        const bool last = last_flag[0] != 0;
-        tc::named_bar_sync(1, 128 * C::kSets);          // (the flag is read before the next item writes it)
-        if (last && ok && o < a.n_out) {
-          __threadfence();
-          const int64_t n = (int64_t)a.n_tok * a.n_out;
-          const int n_mine = min(n_here, C::kCols);
-          for (int e = 0; e < n_mine; ++e) {
-            const float* pr = a.part + (int64_t)(t0 + c_lo + e) * a.n_out + o;
-            float s = 0.f;
-            for (int p0 = 0; p0 < a.splits; p0 += 16) {
-              float v[16];
+    for (int d = 0; d < C::kAhead; ++d) load(v[d]);
+    for (int j0 = 0; j0 < total && ok; j0 += C::kAhead) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = p0 + j < a.splits ? __ldcg(pr + (p0 + j) * n) : 0.f;
+      for (int d = 0; d < C::kAhead; ++d) {
+        const uint32_t x = (uint32_t)(j0 + d);
+        if (j0 + d < total && ok) {
+          if (x >= (uint32_t)S) ok = tc::mbar_wait(&empty[x % S], ((x / S) - 1) & 1, kLimit) && !*abort_flag;
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            uint8_t* st = sm + (size_t)(x % S) * C::kStageBytes;
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (p0 + j < a.splits) s = p0 + j == 0 ? v[j] : s + v[j];
-            }
-            g_store(y, y0 + (int64_t)e * rows, bf, s);
+            for (int i = 0; i < C::kUnits; ++i)
+              if (i < n_units) {
+                uint4 codes;
+                const uint32_t sf = quant_unit(v[d][i], codes);
+                const int r = r0 + 16 * i;
+                *reinterpret_cast<uint4*>(st + kXOff + code_off(r, c)) = codes;
+                if (c == 0) *reinterpret_cast<uint32_t*>(st + kXsfOff + scale_off(r)) = sf;
+              }
+            tc::fence_proxy_async_smem();               // (the MMA reads them through the async proxy)
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&full[x % S]);
+            load(v[d]);
           }
         }
       }
     }
     if (!ok) *abort_flag = 1;
+  } else {
+    // ---- epilogue
+    tc::griddep_wait();                                 // outputs may be written
+    const int q4 = warp & 3, set = (warp - 2) >> 2;
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    const int c_lo = set * C::kCols;
+    uint32_t u = 0;
+    for (int it = it0; it < a.tiles; it += it_step) {
+      const int rt = it / a.tok_tiles, tt = it % a.tok_tiles;
+      const int o = rt * kRowTile + q4 * 32 + lane;
+      const int t0 = tt * a.tile_n;
+      const int n_here = min(a.tile_n, a.n_tok - t0) - c_lo;      // this set's tokens (may be <= 0)
+      // The columns go out 16 at a time: to the outputs, or (spread) as this
+      // part's sums to the ring's memory, where nothing is in flight any
+      // more, as [token][feature].
+      float* pw = reinterpret_cast<float*>(sm) + c_lo * kRowTile + q4 * 32 + lane;
+      const OutRow y = out_row(a.out, o < a.n_out ? o : 0);
+      auto emit = [&](int c0, const float* v) {
+        if (a.spread) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (c0 + e < n_here) pw[(c0 + e) * kRowTile] = v[e];
+        } else if (o < a.n_out) {
+          y.store16(t0 + c_lo + c0, n_here - c0, v);
+        }
+      };
+      if (FUSE || q1 - q0 == 1) {
+        ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit) && !*abort_flag;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        tc::tc_fence_after();
+        for (int c0 = 0; c0 < C::kCols && c0 < n_here; c0 += 16) {
+          uint32_t v[16];
+          tc::tmem_ld_x16(tmem + lane_base + (u & 1) * NT + c_lo + c0, v);
+          tc::tmem_wait_ld();
+          emit(c0, reinterpret_cast<const float*>(v));
+        }
+        tc::tc_fence_before();
+        tc::mbar_arrive(&acc_empty[u & 1]);
+        ++u;
+      } else {
+        float acc[C::kCols];
+        for (int q = q0; q < q1; ++q, ++u) {
+          ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit) && !*abort_flag;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
+          tc::tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < C::kCols; c0 += 16) {
+            if (c0 < n_here) {
+              uint32_t v[16];
+              tc::tmem_ld_x16(tmem + lane_base + (u & 1) * NT + c_lo + c0, v);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                acc[c0 + e] = q == q0 ? __uint_as_float(v[e]) : acc[c0 + e] + __uint_as_float(v[e]);
+            }
+          }
+          tc::tc_fence_before();
+          tc::mbar_arrive(&acc_empty[u & 1]);
+        }
+        if (!ok) continue;
+#pragma unroll
+        for (int c0 = 0; c0 < C::kCols; c0 += 16)
+          if (c0 < n_here) emit(c0, acc + c0);
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  if (a.spread) {
+    // Every CTA of the cluster adds the parts, in part order, of the tokens
+    // part, part + S, ...
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const int et = tid - 64;
+    const int rt = it0 / a.tok_tiles, t0 = (it0 % a.tok_tiles) * a.tile_n;
+    const int f = et & (kRowTile - 1), o = rt * kRowTile + f;
+    if (et >= 0 && et < C::kEpi && o < a.n_out && !*abort_flag) {
+      const int n_here = min(a.tile_n, a.n_tok - t0);
+      const OutRow y = out_row(a.out, o);
+      const float* src[kMaxParts];
+#pragma unroll
+      for (int p = 0; p < kMaxParts; ++p)
+        src[p] = cluster.map_shared_rank(reinterpret_cast<float*>(sm), p < a.splits ? p : 0) + f;
+      for (int e = part + a.splits * (et / kRowTile); e < n_here; e += a.splits * C::kSets) {
+        float v[kMaxParts];
+#pragma unroll
+        for (int p = 0; p < kMaxParts; ++p) v[p] = p < a.splits ? src[p][e * kRowTile] : 0.f;
+        float s = v[0];
+#pragma unroll
+        for (int p = 1; p < kMaxParts; ++p)
+          if (p < a.splits) s += v[p];
+        y.store(t0 + e, s);
+      }
+    }
+    cluster.sync();                                     // a CTA's memory stays until every other has read it
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -468,6 +591,8 @@ __global__ void __launch_bounds__(256) fp8_pack_w_kernel(const uint8_t* codes, c
   }
 }
 
+__global__ void fp8_pack_end_kernel() {}
+
 // BF16 weight [n_out][kg] -> E4M3 codes and one E8M0 scale per 128 x 128
 // block, by the rule of fp8_exponent; a block that holds an infinity or a NaN
 // gets the NaN scale.
@@ -486,7 +611,7 @@ __global__ void __launch_bounds__(256) fp8_quant_w_kernel(const uint16_t* w, int
   __syncthreads();
   top = s_top;
   const bool finite = top < 0x7F80u;
-  const int e = finite ? fp8_exponent(bf16_val((uint16_t)top)) : 0;
+  const int e = finite ? fp8_exponent(top) : 0;
   for (int u = threadIdx.x; u < kRowTile * kKBlk; u += blockDim.x) {
     const int o = rt * kRowTile + u / kKBlk, k = kb * kKBlk + u % kKBlk;
     if (o < n_out && k < kg)
@@ -500,16 +625,16 @@ __global__ void __launch_bounds__(256) fp8_quant_w_kernel(const uint16_t* w, int
 namespace {
 
 struct Plan {
-  int row_tiles, k_blocks, sup, splits, nt, tok_tiles, tile_n, chunks, spread, items;
-  size_t xp, xsf, part, done, total;      // workspace offsets and size
+  int row_tiles, k_blocks, sup, splits, nt, tok_tiles, tile_n, chunks, tiles;
+  bool fuse, spread;
+  size_t xp, xsf, total;      // workspace offsets and size
 };
 
 // K parts of a weight: a function of its shape and the device alone.  As many
-// as give every SM two work items of a few-token call, each at least
-// kMinPartBlocks blocks long.
+// as give every SM two CTAs of a few-token call, each at least
+// kMinPartBlocks blocks long, and no more than a cluster holds.
 int fp8_splits(int row_tiles, int k_blocks, int sms) {
-  int s = 2 * sms / row_tiles;
-  if (s > k_blocks / kMinPartBlocks) s = k_blocks / kMinPartBlocks;
+  const int s = std::min(std::min(2 * sms / row_tiles, k_blocks / kMinPartBlocks), kMaxParts);
   return s < 1 ? 1 : s;
 }
 
@@ -519,49 +644,62 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
   p.k_blocks = (k_in / groups + kKBlk - 1) / kKBlk;
   p.sup = (p.k_blocks + 3) / 4;
   p.splits = fp8_splits(p.row_tiles, p.k_blocks, sms);
-  p.nt = n_tok <= 32 ? 32 : n_tok <= 64 ? 64 : n_tok <= 128 ? 128 : 224;
-  p.tok_tiles = (n_tok + p.nt - 1) / p.nt;
-  // equal tiles, in steps of 32 tokens
-  p.tile_n = ((n_tok + p.tok_tiles - 1) / p.tok_tiles + 31) / 32 * 32;
+  p.fuse = n_tok <= kFuseTokens;
+  if (p.fuse) {
+    p.nt = (n_tok + 15) / 16 * 16;
+    p.tok_tiles = 1;
+    p.tile_n = p.nt;
+  } else {
+    // the largest token tiles that still give every SM one; tiles of one call
+    // are equal, in steps of 16 tokens
+    for (int nt : {224, 128, 64}) {
+      p.nt = nt;
+      p.tok_tiles = (n_tok + nt - 1) / nt;
+      if ((int64_t)p.row_tiles * p.tok_tiles >= sms) break;
+    }
+    p.tile_n = ((n_tok + p.tok_tiles - 1) / p.tok_tiles + 15) / 16 * 16;
+  }
   p.chunks = (p.tile_n + 127) / 128;
-  p.spread = p.row_tiles * (int64_t)p.tok_tiles < sms ? 1 : 0;
-  p.items = p.row_tiles * p.tok_tiles * (p.spread ? p.splits : 1);
+  p.tiles = p.row_tiles * p.tok_tiles;
+  // one CTA per part where whole tiles would leave half of the SMs idle
+  p.spread = p.splits > 1 && (p.fuse || 2 * p.tiles <= sms);
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
-  size_t o = 0;
-  p.xp = o;   o += al((size_t)groups * p.k_blocks * p.tok_tiles * p.tile_n * kKBlk);
-  p.xsf = o;  o += al((size_t)groups * p.sup * p.tok_tiles * p.chunks * kSfBytes);
-  const bool partial = p.spread && p.splits > 1;
-  p.part = o; o += al(partial ? (size_t)p.splits * n_tok * n_out * 4 : 0);
-  p.done = o; o += al(partial ? (size_t)p.row_tiles * p.tok_tiles * 4 : 0);
-  p.total = o;
+  if (!p.fuse) {
+    p.xp = 0;
+    p.xsf = al((size_t)groups * p.k_blocks * p.tok_tiles * p.tile_n * kKBlk);
+    p.total = p.xsf + al((size_t)groups * p.sup * p.tok_tiles * p.chunks * kSfBytes);
+  }
   return p;
 }
 
-template <int NT>
+template <int NT, bool FUSE>
 cudaError_t launch_nt(const Fp8Args& a, int sms, cudaStream_t st) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, FUSE>;
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (setup_needed(attr_set, dev)) {
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    e = cudaFuncSetAttribute(fp8_gemm_kernel<NT, FUSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<NT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    e = cudaFuncSetAttribute(fp8_gemm_kernel<NT, FUSE>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
     setup_done(attr_set, dev);
   }
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)(a.items < sms * C::kPerSm ? a.items : sms * C::kPerSm));
+  lc.gridDim = dim3((unsigned)(a.spread ? a.tiles * a.splits : std::min(a.tiles, sms * C::kPerSm)));
   lc.blockDim = dim3(C::kThreads);
   lc.dynamicSmemBytes = C::kSmem;
   lc.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)a.splits;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   lc.attrs = at;
-  lc.numAttrs = 1;
-  e = cudaLaunchKernelEx(&lc, fp8_gemm_kernel<NT>, a);
+  lc.numAttrs = a.spread ? 2 : 1;
+  e = cudaLaunchKernelEx(&lc, fp8_gemm_kernel<NT, FUSE>, a);
   note_launch();
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -585,6 +723,12 @@ cudaError_t launch_fp8_pack_weight(const uint8_t* codes, const uint8_t* scales, 
   fp8_pack_w_kernel<<<dim3(kb, rt), 256, 0, st>>>(codes, scales, n_out, kg, kb, (kb + 3) / 4, aligned, w,
                                                   w + (size_t)rt * kb * kWTileBytes);
   note_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // The product reads the weight before it waits for the kernel ahead of it
+  // on the stream: that kernel must not be the packing itself.
+  fp8_pack_end_kernel<<<1, 32, 0, st>>>();
+  note_launch();
   return cudaGetLastError();
 }
 
@@ -601,37 +745,49 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   const Plan p = fp8_plan(n_out, k_in, groups, n_tok, sms);
   uint8_t* base = static_cast<uint8_t*>(ws);
   const uint8_t* w = static_cast<const uint8_t*>(w_packed);
-  const bool partial = p.spread && p.splits > 1;
-  int32_t* done = partial ? reinterpret_cast<int32_t*>(base + p.done) : nullptr;
   const int kg = k_in / groups;
-  const int64_t units = (int64_t)p.k_blocks * p.tok_tiles * p.tile_n * 8;
-  const int blocks = (int)std::min<int64_t>((units + 255) / 256, 8 * sms);
-  // aligned: every row of every group starts on 16 bytes (kg is a multiple of 8)
+  // every row of every group starts on 16 bytes (kg is a multiple of 8)
   const bool aligned = reinterpret_cast<uintptr_t>(x) % 16 == 0;
-  fp8_quant_x_kernel<<<dim3(blocks, groups), 256, 0, st>>>(x, n_tok, kg, (int64_t)k_in, p.k_blocks, p.sup, p.tok_tiles,
-                                                           p.tile_n, p.chunks, aligned, base + p.xp, base + p.xsf, done,
-                                                           p.row_tiles * p.tok_tiles);
-  note_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   Fp8Args a{};
   a.w = w;
   a.wsf = w + (size_t)p.row_tiles * p.k_blocks * kWTileBytes;
-  a.xp = base + p.xp;
-  a.xsf = base + p.xsf;
+  a.x = x;
+  a.x_aligned = aligned;
+  a.kg = kg;
   a.n_out = n_out; a.n_tok = n_tok;
   a.row_tiles = p.row_tiles; a.k_blocks = p.k_blocks; a.sup = p.sup;
   a.groups = groups; a.splits = p.splits;
   a.tok_tiles = p.tok_tiles; a.tile_n = p.tile_n;
-  a.spread = p.spread; a.items = p.items;
+  a.spread = p.spread; a.tiles = p.tiles;
   a.out = out;
-  a.part = partial ? reinterpret_cast<float*>(base + p.part) : nullptr;
-  a.done = done;
+  if (p.fuse) {
+    switch (p.nt) {
+      case 16: return launch_nt<16, true>(a, sms, st);
+      case 32: return launch_nt<32, true>(a, sms, st);
+      case 48: return launch_nt<48, true>(a, sms, st);
+      default: return launch_nt<64, true>(a, sms, st);
+    }
+  }
+  a.xp = base + p.xp;
+  a.xsf = base + p.xsf;
+  const int64_t units = (int64_t)p.k_blocks * p.tok_tiles * p.tile_n * 8;
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3((unsigned)std::min<int64_t>((units + 255) / 256, 8 * sms), (unsigned)groups);
+  lc.blockDim = dim3(256);
+  lc.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&lc, fp8_quant_x_kernel, x, n_tok, kg, (int64_t)k_in, p.k_blocks, p.sup, p.tok_tiles,
+                                     p.tile_n, p.chunks, aligned, base + p.xp, base + p.xsf);
+  note_launch();
+  if (e != cudaSuccess) return e;
   switch (p.nt) {
-    case 32: return launch_nt<32>(a, sms, st);
-    case 64: return launch_nt<64>(a, sms, st);
-    case 128: return launch_nt<128>(a, sms, st);
-    default: return launch_nt<224>(a, sms, st);
+    case 64: return launch_nt<64, false>(a, sms, st);
+    case 128: return launch_nt<128, false>(a, sms, st);
+    default: return launch_nt<224, false>(a, sms, st);
   }
 }
 

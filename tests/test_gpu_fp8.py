@@ -242,11 +242,12 @@ def test_two_streams_and_two_graphs_do_not_share_scratch():
 
 
 def test_an_own_workspace_and_an_empty_batch():
-    x, _, codes, scales = _inputs(2368, 1536, 1, 12, 23)
+    x, _, codes, scales = _inputs(2368, 1536, 1, 100, 23)
     lin = _linear(codes, scales)
-    y, z = torch.empty((12, 2368), device="cuda"), torch.full((12, 2368), 5.0, device="cuda")
+    y, z = torch.empty((100, 2368), device="cuda"), torch.full((100, 2368), 5.0, device="cuda")
+    assert lin.workspace_bytes(64) == 0
     lin(x.cuda(), y)
-    ws = torch.full((lin.workspace_bytes(12) + 256,), 0xAB, dtype=torch.uint8, device="cuda")
+    ws = torch.full((lin.workspace_bytes(100) + 256,), 0xAB, dtype=torch.uint8, device="cuda")
     lin(x.cuda(), z, workspace=ws)
     assert torch.equal(y, z)
     with pytest.raises(RuntimeError, match="workspace smaller"):
