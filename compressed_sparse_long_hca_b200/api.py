@@ -8,7 +8,6 @@ from __future__ import annotations
 
 import ctypes
 import struct
-from contextlib import nullcontext
 
 import numpy as np
 import torch
@@ -653,20 +652,31 @@ class Linear:
         check(_lib.load().csa_gemm_check_device_error(_stream(stream)), "gemm device")
 
 
-def _current_device(device: torch.device):
-    """A context in which `device` is the current CUDA device (none when it
-    is already)."""
-    return nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _raw_stream(stream, index: int) -> int | None:
+    """The handle of `stream`, or of device `index`'s current stream
+    (torch.cuda.current_stream makes a Stream object: 3 us of host time)."""
+    return (torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream) or None
+
+
+def _on_device(index: int, call, *args) -> int:
+    """call(*args) with CUDA device `index` current."""
+    if torch.cuda.current_device() == index:
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
 
 
 def _scratch(nbytes: int, device: torch.device, stream) -> torch.Tensor:
     """Scratch for one call on `stream`, from the allocator of that stream:
     calls on different streams, and graphs captured one by one, never share
     it.  The allocator reuses it only behind the work queued so far."""
-    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+_GEMM_OUT = struct.Struct("@iiP")                    # csa_gemm_out
 
 
 class LinearFP8:
@@ -702,11 +712,11 @@ class LinearFP8:
         _need(scales, torch.uint8, (-(-self.n_out // 128), -(-kg // 128)), "scales")
         if scales.device != self.device:
             raise ValueError("codes and scales must be on one device")
-        with _current_device(self.device):
-            self.packed = _scratch(nbytes, self.device, stream)
-            check(self.lib.csa_gemm_fp8_pack_weight(_ptr(codes), _ptr(scales), self.n_out, self.k_in, self.groups,
-                                                    self.packed.data_ptr(), nbytes, _stream(stream)),
-                  "csa_gemm_fp8_pack_weight")
+        self._index = self.device.index
+        self.packed = _scratch(nbytes, self.device, stream)
+        check(_on_device(self._index, self.lib.csa_gemm_fp8_pack_weight, _ptr(codes), _ptr(scales), self.n_out, self.k_in,
+                         self.groups, self.packed.data_ptr(), nbytes, _raw_stream(stream, self._index)),
+              "csa_gemm_fp8_pack_weight")
         self._need_bytes = {}
 
     @classmethod
@@ -720,46 +730,50 @@ class LinearFP8:
     def workspace_bytes(self, n_tok: int) -> int:
         need = self._need_bytes.get(n_tok)
         if need is None:
-            with _current_device(self.device):
-                need = int(self.lib.csa_gemm_fp8_workspace_bytes(self.n_out, self.k_in, self.groups, n_tok))
+            need = int(_on_device(self._index, self.lib.csa_gemm_fp8_workspace_bytes, self.n_out, self.k_in, self.groups,
+                                  n_tok))
             self._need_bytes[n_tok] = need
         return need
 
     def __call__(self, x: torch.Tensor, outs, workspace: torch.Tensor | None = None, stream=None):
         """x: CUDA BF16 [n_tok][k_in].  outs: one tensor or a list of CUDA
         tensors [n_tok][rows_s] (BF16 or fp32, contiguous) whose rows add up
-        to n_out, as Linear's.  A call of more than 64 tokens needs scratch:
+        to n_out, as Linear's.  A call of more than 16 tokens needs scratch:
         unless `workspace` is given, it takes its own from the allocator.
         Returns outs."""
-        segs = [outs] if isinstance(outs, torch.Tensor) else outs
-        n = x.shape[0] if x.dim() == 2 else -1
-        _need(x, torch.bfloat16, (n, self.k_in), "x")
-        arr = (_lib.GemmOut * len(segs))()
-        for s, t in enumerate(segs):
-            bf16 = t.dtype == torch.bfloat16
-            _need(t, torch.bfloat16 if bf16 else torch.float32, (n, t.shape[1] if t.dim() == 2 else -1), f"outs[{s}]")
-            if t.device != self.device:
-                raise ValueError("outputs must be on the weight's device")
-            arr[s].rows, arr[s].bf16, arr[s].y = t.shape[1], bf16, t.data_ptr()
-        if x.device != self.device:
-            raise ValueError("x must be on the weight's device")
+        index = self._index
+        if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.k_in \
+                or x.get_device() != index or not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous BF16 matrix [n_tok, {self.k_in}] on {self.device}")
+        n = x.shape[0]
+        segs, n_seg = b"", 0
+        for t in (outs,) if isinstance(outs, torch.Tensor) else outs:
+            dt, shape = t.dtype, t.shape
+            bf16 = dt is torch.bfloat16
+            if not bf16 and dt is not torch.float32 or len(shape) != 2 or shape[0] != n or t.get_device() != index \
+                    or not t.is_contiguous():
+                raise ValueError(f"outs[{n_seg}] must be a contiguous BF16 or fp32 matrix [{n}, rows] on {self.device}")
+            segs += _GEMM_OUT.pack(shape[1], bf16, t.data_ptr())
+            n_seg += 1
         if n == 0:
             return outs
-        with _current_device(self.device):
+        at = size = 0
+        if workspace is None:
             need = self.workspace_bytes(n)
-            if workspace is not None:
-                _need(workspace, torch.uint8, name="workspace")
-                if workspace.device != self.device:
-                    raise ValueError("workspace must be on the weight's device")
-            elif need:
+            if need:
                 workspace = _scratch(need + 256, self.device, stream)
-            at = ws = size = 0
-            if workspace is not None:
-                at = workspace.data_ptr()
-                ws = (at + 255) // 256 * 256
-                size = workspace.numel() - (ws - at)
-            check(self.lib.csa_gemm_fp8(self.packed.data_ptr(), self.n_out, self.k_in, self.groups, x.data_ptr(), n,
-                                        len(segs), arr, ws, size, _stream(stream)), "csa_gemm_fp8")
+        else:
+            _need(workspace, torch.uint8, name="workspace")
+            if workspace.device != self.device:
+                raise ValueError("workspace must be on the weight's device")
+        if workspace is not None:
+            base = workspace.data_ptr()
+            at = (base + 255) // 256 * 256
+            size = workspace.numel() - (at - base)
+        status = _on_device(index, self.lib.csa_gemm_fp8, self.packed.data_ptr(), self.n_out, self.k_in, self.groups,
+                            x.data_ptr(), n, n_seg, segs, at, size, _raw_stream(stream, index))
+        if status:
+            check(status, "csa_gemm_fp8")
         return outs
 
     @staticmethod
@@ -781,11 +795,10 @@ def quantize_fp8_weight(w, device: str | torch.device = "cuda", stream=None):
         w = w.to(device)
     w = w.to(torch.bfloat16).contiguous()
     n_out, k = (int(v) for v in w.shape)
-    with _current_device(w.device):
-        codes = torch.empty((n_out, k), dtype=torch.uint8, device=w.device)
-        scales = torch.empty((-(-n_out // 128), -(-k // 128)), dtype=torch.uint8, device=w.device)
-        check(_lib.load().csa_gemm_fp8_quant_weight(_ptr(w), n_out, k, 1, _ptr(codes), _ptr(scales), _stream(stream)),
-              "csa_gemm_fp8_quant_weight")
+    codes = torch.empty((n_out, k), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((-(-n_out // 128), -(-k // 128)), dtype=torch.uint8, device=w.device)
+    check(_on_device(w.device.index, _lib.load().csa_gemm_fp8_quant_weight, _ptr(w), n_out, k, 1, _ptr(codes), _ptr(scales),
+                     _raw_stream(stream, w.device.index)), "csa_gemm_fp8_quant_weight")
     return codes.view(torch.float8_e4m3fn), scales
 
 
@@ -823,25 +836,32 @@ class HeadNorm:
         self.q_weight, self.k_weight = weight(q_weight, "q_weight"), weight(k_weight, "k_weight")
         theta = float(rope_base) ** (-2.0 * np.arange(self.rope // 2, dtype=np.float64) / max(self.rope, 1))
         self.theta = torch.from_numpy(theta).to(device)
+        if not self.theta.is_cuda:
+            raise ValueError("device must be a CUDA device")
         self.device = self.theta.device
+        self._index = self.device.index
+        self._theta = self.theta.data_ptr()
+        self._q_weight, self._k_weight = (0 if w is None else w.data_ptr() for w in (self.q_weight, self.k_weight))
+        self.rotate_k = self.rotate_k and self.rope > 0
 
-    def _part(self, x, y, weight, rotate, n, name):
+    def _part(self, x, y, weight, rotate, n, name) -> bytes:
         """The packed csa_head_norm_part of heads x and their output y."""
-        if not isinstance(x, torch.Tensor) or not isinstance(y, torch.Tensor) or x.device != self.device \
-                or y.device != self.device:
-            raise ValueError(f"{name} and {name}_out must be tensors on {self.device}")
-        dt = x.dtype
-        if dt != torch.bfloat16 and dt != torch.float32:
-            raise ValueError(f"{name} must be BF16 or fp32")
-        if x.dim() != 3 or x.shape[0] != n or x.shape[2] != self.dim:
-            raise ValueError(f"{name} must have shape ({n}, heads, {self.dim}), got {tuple(x.shape)}")
-        if y.dtype != dt or y.shape != x.shape:
-            raise ValueError(f"{name}_out must have {name}'s type and shape")
-        (xt, xh, xd), (yt, yh, yd) = x.stride(), y.stride()
+        if not isinstance(x, torch.Tensor) or not isinstance(y, torch.Tensor):
+            raise ValueError(f"{name} and {name}_out must be tensors")
+        dt, shape = x.dtype, x.shape
+        f32 = dt is torch.float32
+        if not f32 and dt is not torch.bfloat16 or len(shape) != 3 or shape[0] != n or shape[2] != self.dim \
+                or x.get_device() != self._index:
+            raise ValueError(f"{name} must be BF16 or fp32 [{n}, heads, {self.dim}] on {self.device}, "
+                             f"got {dt} {tuple(shape)} on {x.device}")
+        xt, xh, xd = yt, yh, yd = x.stride()
+        if y is not x:
+            if y.dtype is not dt or y.shape != shape or y.get_device() != self._index:
+                raise ValueError(f"{name}_out must have {name}'s type, shape and device")
+            yt, yh, yd = y.stride()
         if (xd != 1 or yd != 1) and x.numel():
             raise ValueError(f"the dims of {name} and {name}_out must be contiguous")
-        return _HEAD_NORM_PART.pack(x.data_ptr(), y.data_ptr(), 0 if weight is None else weight.data_ptr(), xt, xh, yt, yh,
-                                    x.shape[1], dt == torch.float32, rotate)
+        return _HEAD_NORM_PART.pack(x.data_ptr(), y.data_ptr(), weight, xt, xh, yt, yh, shape[1], f32, rotate)
 
     def __call__(self, positions, q, q_out=None, k=None, k_out=None, stream=None):
         """q: CUDA BF16 or fp32 [n, heads, dim], k: the same or None (its own
@@ -853,17 +873,18 @@ class HeadNorm:
         n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else -1
         q_out = q if q_out is None else q_out
         k_out = k if k_out is None else k_out
-        part = self._part(q, q_out, self.q_weight, self.rope > 0, n, "q")
-        k_part = None if k is None else self._part(k, k_out, self.k_weight, self.rotate_k and self.rope > 0, n, "k")
+        part = self._part(q, q_out, self._q_weight, self.rope > 0, n, "q")
+        k_part = None if k is None else self._part(k, k_out, self._k_weight, self.rotate_k, n, "k")
         pos = None
         if positions is not None or self.rope:
-            _need(positions, torch.int64, (n,), "positions")
-            if positions.device != self.device:
-                raise ValueError(f"positions must be on {self.device}")
+            if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int64 or positions.dim() != 1 \
+                    or positions.shape[0] != n or positions.get_device() != self._index or not positions.is_contiguous():
+                raise ValueError(f"positions must be contiguous int64 [{n}] on {self.device}")
             pos = positions.data_ptr()
-        with _current_device(self.device):
-            check(self.lib.csa_head_norm(n, self.dim, self.rope, self.eps, pos, self.theta.data_ptr(), part, k_part,
-                                         _stream(stream)), "csa_head_norm")
+        status = _on_device(self._index, self.lib.csa_head_norm, n, self.dim, self.rope, self.eps, pos, self._theta, part,
+                            k_part, _raw_stream(stream, self._index))
+        if status:
+            check(status, "csa_head_norm")
         return q_out, k_out
 
 

@@ -33,11 +33,12 @@
 // The K order inside a part is fixed and a token's column does not enter the
 // arithmetic of the others, so a token's bits depend on its row and the weight.
 //
-// Up to 64 tokens (a weight stream) the call is one launch without scratch:
-// four warps of each CTA quantise the tokens' block of every stage from global
-// memory straight into the MMA's operand layout, a few blocks ahead.  Beyond
-// that the quantised tokens are worth keeping: a kernel packs them once, and
-// the product's CTAs read blocks of them by bulk copies.
+// Up to 16 tokens (a weight stream) the call is one launch without scratch:
+// four warps of each CTA quantise the tokens' blocks from global memory
+// straight into the MMA's operand layout.  Beyond that the quantised tokens
+// are worth keeping: a kernel packs them once, and the product's CTAs read
+// blocks of them by bulk copies (7168 x 16384, 37 tokens: 46 us with the
+// tokens quantised in every CTA, 29 us packed; 20 tokens 34 and 26 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -62,7 +63,7 @@ constexpr int kSfBytes = 512;                 // scales of 128 rows x 4 blocks, 
 constexpr int kSfRing = 4;                    // scale buffers in TMEM
 constexpr int kMinPartBlocks = 4;             // K blocks of the smallest part
 constexpr int kMaxParts = 8;                  // parts of a weight: CTAs of the largest portable cluster
-constexpr int kFuseTokens = 64;               // most tokens that the product quantises itself
+constexpr int kFuseTokens = 16;               // most tokens that the product quantises itself
 
 struct Fp8Args {
   const uint8_t* w;       // packed weight: tiles [row_tiles][k_blocks][16 KB]
@@ -93,8 +94,7 @@ struct Cfg {
   static constexpr int kStageBytes = kWTileBytes + NT * kKBlk + kSfBytes * (1 + kChunks);
   static constexpr int kStagesFit = (kPerSm == 2 ? 110 : 224) * 1024 / kStageBytes;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
-  static constexpr int kUnits = NT / 16;                   // fused: 16-value units of a thread per block
-  static constexpr int kAhead = NT <= 16 ? 6 : NT <= 32 ? 3 : NT <= 48 ? 2 : 1;   // blocks it loads ahead (48 registers)
+  static constexpr int kBatch = 4;                         // fused: blocks a thread loads at once (32 registers)
   // TMEM: two accumulators, the weight's scale ring, the tokens' scale ring
   static constexpr uint32_t kXsfRing = FUSE ? 8 : kSfRing;
   static constexpr uint32_t kWsfBase = 2 * NT, kXsfBase = kWsfBase + 4 * kSfRing;
@@ -102,7 +102,8 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
   static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 256 + 128;
   static_assert(kColsNeeded <= 512 && kTmemCols * kPerSm <= 512, "TMEM");
-  static_assert(kStages >= 3 && kStages <= 8, "stages");
+  static_assert(kStages >= 3 && kStages <= 8 && kBatch <= kStages, "stages");
+  static_assert(!FUSE || NT == 16, "a quantising thread takes one unit of a block");
   static_assert(kRowTile * NT * 4 <= kStages * kStageBytes, "a part's sums fit in the ring");
 };
 
@@ -391,55 +392,49 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
     }
     if (!ok) *abort_flag = 1;
   } else if (FUSE && warp >= 2 + C::kEpi / 32) {
-    // ---- token quantiser: block after block of this CTA's tiles, the loads
-    //      kAhead blocks before their use
+    // ---- token quantiser: the blocks of this CTA's tiles, kBatch at a time: all
+    //      their loads in flight together, one proxy fence for all (a fence
+    //      waits for the loads in flight, so that loading ahead across it
+    //      gains nothing)
     tc::griddep_wait();
-    const int qt = tid - 64 - C::kEpi;                  // unit: row (qt >> 5) * 4 + (qt & 3) + 16 i, column (qt >> 2) & 7
-    const int r0 = (qt >> 5) * 4 + (qt & 3), c = (qt >> 2) & 7;
-    const int n_units = a.tile_n / 16;
+    const int qt = tid - 64 - C::kEpi;                  // row (qt >> 5) * 4 + (qt & 3), column (qt >> 2) & 7
+    const int r = (qt >> 5) * 4 + (qt & 3), c = (qt >> 2) & 7;
     const int64_t row_len = (int64_t)a.groups * a.kg;
     const int n_it = it0 < a.tiles ? (a.tiles - 1 - it0) / it_step + 1 : 0;
     const int total = n_it * (k1 - k0);
     int lit = it0, lkb = k0;                            // the next block to load
-    Unit v[C::kAhead][C::kUnits];
-    auto load = [&](Unit (&dst)[C::kUnits]) {
+    Unit v[C::kBatch];
+    auto load = [&](Unit& dst) {
       const int64_t grp = (lit * kRowTile) / rows_per_group;
       const int col = lkb * kKBlk + c * 16;
-      const uint16_t* p = a.x + grp * a.kg + col;
-#pragma unroll
-      for (int i = 0; i < C::kUnits; ++i) {
-        const int t = r0 + 16 * i;
-        const bool there = lit < a.tiles && i < n_units && t < a.n_tok;
-        dst[i] = load_unit(p + (int64_t)(there ? t : 0) * row_len, there ? a.kg - col : 0, a.x_aligned != 0);
-      }
+      const bool there = lit < a.tiles && r < a.n_tok;
+      dst = load_unit(a.x + (there ? r : 0) * row_len + grp * a.kg + col, there ? a.kg - col : 0, a.x_aligned != 0);
       if (++lkb == k1) { lkb = k0; lit += it_step; }
     };
+    for (int j0 = 0; j0 < total && ok; j0 += C::kBatch) {
 #pragma unroll
-    for (int d = 0; d < C::kAhead; ++d) load(v[d]);
-    for (int j0 = 0; j0 < total && ok; j0 += C::kAhead) {
+      for (int d = 0; d < C::kBatch; ++d) load(v[d]);   // (past the last block: zeros, not used)
 #pragma unroll
-      for (int d = 0; d < C::kAhead; ++d) {
+      for (int d = 0; d < C::kBatch; ++d) {
         const uint32_t x = (uint32_t)(j0 + d);
         if (j0 + d < total && ok) {
           if (x >= (uint32_t)S) ok = tc::mbar_wait(&empty[x % S], ((x / S) - 1) & 1, kLimit) && !*abort_flag;
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             uint8_t* st = sm + (size_t)(x % S) * C::kStageBytes;
-#pragma unroll
-            for (int i = 0; i < C::kUnits; ++i)
-              if (i < n_units) {
-                uint4 codes;
-                const uint32_t sf = quant_unit(v[d][i], codes);
-                const int r = r0 + 16 * i;
-                *reinterpret_cast<uint4*>(st + kXOff + code_off(r, c)) = codes;
-                if (c == 0) *reinterpret_cast<uint32_t*>(st + kXsfOff + scale_off(r)) = sf;
-              }
-            tc::fence_proxy_async_smem();               // (the MMA reads them through the async proxy)
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&full[x % S]);
-            load(v[d]);
+            uint4 codes;
+            const uint32_t sf = quant_unit(v[d], codes);
+            *reinterpret_cast<uint4*>(st + kXOff + code_off(r, c)) = codes;
+            if (c == 0) *reinterpret_cast<uint32_t*>(st + kXsfOff + scale_off(r)) = sf;
           }
         }
+      }
+      if (ok) {
+        tc::fence_proxy_async_smem();                   // (the MMA reads them through the async proxy)
+        __syncwarp();
+#pragma unroll
+        for (int d = 0; d < C::kBatch; ++d)
+          if (lane == 0 && j0 + d < total) tc::mbar_arrive(&full[(uint32_t)(j0 + d) % S]);
       }
     }
     if (!ok) *abort_flag = 1;
@@ -630,12 +625,15 @@ struct Plan {
   size_t xp, xsf, total;      // workspace offsets and size
 };
 
-// K parts of a weight: a function of its shape and the device alone.  As many
-// as give every SM two CTAs of a few-token call, each at least
-// kMinPartBlocks blocks long, and no more than a cluster holds.
+// K parts of a weight: a function of its shape and the device alone.  The
+// power of two that gives the SMs two CTAs each, every part at least
+// kMinPartBlocks blocks long; 7/8 of the places count, for a cluster lies
+// within a group of 16 to 20 SMs and those are not filled to the last place
+// (56 clusters of 5 ran as two waves: 40 us instead of 26).
 int fp8_splits(int row_tiles, int k_blocks, int sms) {
-  const int s = std::min(std::min(2 * sms / row_tiles, k_blocks / kMinPartBlocks), kMaxParts);
-  return s < 1 ? 1 : s;
+  int s = 1;
+  while (2 * s <= kMaxParts && 16 * s * row_tiles <= 14 * sms && 2 * s * kMinPartBlocks <= k_blocks) s *= 2;
+  return s;
 }
 
 Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
@@ -646,15 +644,15 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
   p.splits = fp8_splits(p.row_tiles, p.k_blocks, sms);
   p.fuse = n_tok <= kFuseTokens;
   if (p.fuse) {
-    p.nt = (n_tok + 15) / 16 * 16;
+    p.nt = p.tile_n = 16;
     p.tok_tiles = 1;
-    p.tile_n = p.nt;
   } else {
-    // the largest token tiles that still give every SM one; tiles of one call
-    // are equal, in steps of 16 tokens
-    for (int nt : {224, 128, 64}) {
-      p.nt = nt;
-      p.tok_tiles = (n_tok + nt - 1) / nt;
+    // the largest token tiles that still give every SM one, none larger than
+    // the tokens need; tiles of one call are equal, in steps of 16 tokens
+    constexpr int kTiles[] = {224, 128, 64, 32};
+    for (int i = n_tok <= 32 ? 3 : n_tok <= 64 ? 2 : n_tok <= 128 ? 1 : 0; i < (n_tok <= 32 ? 4 : 3); ++i) {
+      p.nt = kTiles[i];
+      p.tok_tiles = (n_tok + p.nt - 1) / p.nt;
       if ((int64_t)p.row_tiles * p.tok_tiles >= sms) break;
     }
     p.tile_n = ((n_tok + p.tok_tiles - 1) / p.tok_tiles + 15) / 16 * 16;
@@ -760,14 +758,7 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   a.tok_tiles = p.tok_tiles; a.tile_n = p.tile_n;
   a.spread = p.spread; a.tiles = p.tiles;
   a.out = out;
-  if (p.fuse) {
-    switch (p.nt) {
-      case 16: return launch_nt<16, true>(a, sms, st);
-      case 32: return launch_nt<32, true>(a, sms, st);
-      case 48: return launch_nt<48, true>(a, sms, st);
-      default: return launch_nt<64, true>(a, sms, st);
-    }
-  }
+  if (p.fuse) return launch_nt<16, true>(a, sms, st);
   a.xp = base + p.xp;
   a.xsf = base + p.xsf;
   const int64_t units = (int64_t)p.k_blocks * p.tok_tiles * p.tile_n * 8;
@@ -785,6 +776,7 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   note_launch();
   if (e != cudaSuccess) return e;
   switch (p.nt) {
+    case 32: return launch_nt<32, false>(a, sms, st);
     case 64: return launch_nt<64, false>(a, sms, st);
     case 128: return launch_nt<128, false>(a, sms, st);
     default: return launch_nt<224, false>(a, sms, st);

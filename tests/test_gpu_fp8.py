@@ -245,7 +245,7 @@ def test_an_own_workspace_and_an_empty_batch():
     x, _, codes, scales = _inputs(2368, 1536, 1, 100, 23)
     lin = _linear(codes, scales)
     y, z = torch.empty((100, 2368), device="cuda"), torch.full((100, 2368), 5.0, device="cuda")
-    assert lin.workspace_bytes(64) == 0
+    assert lin.workspace_bytes(16) == 0
     lin(x.cuda(), y)
     ws = torch.full((lin.workspace_bytes(100) + 256,), 0xAB, dtype=torch.uint8, device="cuda")
     lin(x.cuda(), z, workspace=ws)
