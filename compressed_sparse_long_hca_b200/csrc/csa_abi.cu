@@ -951,7 +951,7 @@ csa_status csa_head_norm(int64_t n_tok, int32_t dim, int32_t rope, double eps, c
     const bool rotate = p->rotate && rope > 0;
     if (rotate && (!positions || !theta)) return fail(CSA_ERR_ARG, "rotated heads need positions and theta");
     a.part[s] = csa::HeadNormPart{p->x, p->y, p->weight, p->x_token_stride, p->x_head_stride, p->y_token_stride,
-                                  p->y_head_stride, p->heads, p->f32 ? 1 : 0, rotate ? 1 : 0, 0, 0, 0};
+                                  p->y_head_stride, p->heads, p->f32 ? 1 : 0, rotate ? 1 : 0, 0, 0, 0, 0};
     heads += p->heads;
   }
   if (heads == 0) return CSA_OK;

@@ -2,16 +2,23 @@
 // (csa_head_norm):
 //     y = w * x / sqrt(mean(x^2) + eps),  then the pairs (2i, 2i+1) of the last
 //     R dims rotated by pos * base^(-2i/R)
-// The sum of squares, the scale and the rotation are fp32, angles fp64 (as in
-// every kernel here: positions reach 2^20); a result is rounded once, to its
-// type.
+// The sum of squares, the scale and the rotation are fp32, angles are reduced
+// in fp64 (positions reach 2^20); a result is rounded once, to its type.
 //
 // Bound: one read and one write of the heads.  A head stays in the registers
 // of the lanes that loaded it (8 values a lane and step; the 2^n lanes that
 // cover the head, so a warp takes four heads of 64 dims, one of 512), so each
 // value moves once each way.  A block works on heads of one token: it loads
-// its first heads, then computes the token's cosines and sines once (fp64, in
-// the shadow of the loads), and every further head reuses them.
+// its first heads, then computes the token's cosines and sines once, in the
+// shadow of the loads, and every further head reuses them; the next heads'
+// loads are issued before the present ones are worked on (4 blocks of 128
+// threads an SM: the registers that the loads in flight take are worth more
+// than more blocks).  4096 tokens x (128 BF16 + 1 fp32) heads of 512 on one
+// B200: 190 us, 5.75 TB/s or 0.88 of a device copy; without the loads ahead
+// 214 us at best (7 blocks), with one value at a time instead of packed fp32
+// pairs and fp64 sines 351 us.
+#include <algorithm>
+
 #include "common.cuh"
 #include "head_norm.cuh"
 #include "tc.cuh"
@@ -23,184 +30,256 @@ namespace {
 constexpr int kHnThreads = 128;
 constexpr int kHnMaxDim = 1024;
 
+// Two fp32 values in one 64-bit register pair, and their packed arithmetic.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Cosine and sine of an angle, each within a few fp32 half steps: the angle in
+// half turns and its reduction in fp64, its fp32 value by sincospif, what that
+// rounding left by the first-order term.
+__device__ __forceinline__ float2 cos_sin(double angle) {
+  const double turns = angle * 0.15915494309189535;      // 1 / (2 pi)
+  const double half = 2.0 * (turns - rint(turns));
+  const float hi = (float)half, lo = (float)((half - (double)hi) * 3.141592653589793);
+  float s, c;
+  sincospif(hi, &s, &c);
+  return make_float2(fmaf(-lo, s, c), fmaf(lo, c, s));
+}
+
+// 8 values of a head as loaded.
 template <typename T>
-struct Raw;                            // 8 values as loaded
+struct Raw;
 template <>
 struct Raw<uint16_t> {
   uint4 v;
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void set(int e, uint16_t b) {
-    uint32_t& w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-    w |= (uint32_t)b << (16 * (e & 1));
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {          // the first n, the others zero
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ float get(int e) const {
-    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-    return bf16_val((uint16_t)(e & 1 ? w >> 16 : w & 0xFFFFu));
+  __device__ __forceinline__ uint64_t get(int i) const {                    // values 2 i, 2 i + 1
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ void store(uint16_t* p, const uint64_t (&y)[4], int n) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpair(y[i]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if (n < 0) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) p[e] = (uint16_t)(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]);
+    }
   }
 };
 template <>
 struct Raw<float> {
-  float4 a, b;
+  uint64_t v[4];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 0;
+  }
   __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = pair(a.x, a.y); v[1] = pair(a.z, a.w); v[2] = pair(b.x, b.y); v[3] = pair(b.z, b.w);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void set(int e, float f) {
-    float4& q = e < 4 ? a : b;
-    ((e & 3) == 0 ? q.x : (e & 3) == 1 ? q.y : (e & 3) == 2 ? q.z : q.w) = f;
+  __device__ __forceinline__ void load(const float* p, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(2 * i < n ? p[2 * i] : 0.f, 2 * i + 1 < n ? p[2 * i + 1] : 0.f);
   }
-  __device__ __forceinline__ float get(int e) const {
-    const float4& q = e < 4 ? a : b;
-    return (e & 3) == 0 ? q.x : (e & 3) == 1 ? q.y : (e & 3) == 2 ? q.z : q.w;
+  __device__ __forceinline__ uint64_t get(int i) const { return v[i]; }
+  static __device__ __forceinline__ void store(float* p, const uint64_t (&y)[4], int n) {
+    const float2 a = unpair(y[0]), b = unpair(y[1]), c = unpair(y[2]), d = unpair(y[3]);
+    if (n < 0) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+      reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+    } else {
+      const float f[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) p[e] = f[e];
+    }
   }
 };
 
-__device__ __forceinline__ void put8(uint16_t* p, const float (&v)[8]) {
-  uint32_t w[4];
+// A head (`wide`) whose squares leave fp32's range: its sum overflowed, or may
+// have lost small squares that eps does not cover.  Its values are scaled by a
+// power of two and summed again, the scale `r` follows in fp64; the warp's
+// other heads stay as they are.  All lanes of the warp call it.
+template <int NC>
+__device__ __forceinline__ void wide_head(uint64_t (&v)[NC][4], float& r, bool wide, int lanes, int dim, double eps) {
+  float top = 0.f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = (uint32_t)bf16_rn(v[2 * e]) | ((uint32_t)bf16_rn(v[2 * e + 1]) << 16);
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpair(v[c][i]);
+      top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+  for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int e = wide && top > 0.f && top <= 3.4028235e38f ? ilogbf(top) : 0;
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpair(v[c][i]);
+      const float x0 = scale_pow2(f.x, e), x1 = scale_pow2(f.y, e);
+      ss = fmaf(x1, x1, fmaf(x0, x0, ss));
+      v[c][i] = pair(x0, x1);
+    }
+  for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (wide) r = (float)(ldexp(1.0, e) / sqrt(ldexp((double)ss / dim, 2 * e) + eps));
 }
-__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void put1(uint16_t* p, float v) { *p = bf16_rn(v); }
-__device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 
-// Heads [h0, h1) of token t.  NC: steps of 8 values a lane takes; U: heads
-// whose loads are in flight at once.
-template <typename T, int NC, int U>
+// Heads h0 + slot, h0 + slot + slots, ... below h1 of token t.  NC: steps of
+// 8 values a lane takes; U: heads whose loads are in flight at once.  kVec:
+// 16-byte accesses.  `table`: the block's cosines and sines still have to be
+// computed (by every warp of the block together).
+template <typename T, int NC, int U, bool kVec>
 __device__ __forceinline__ void norm_heads(const HeadNormArgs& a, const HeadNormPart& p, int64_t t, int h0, int h1,
-                                           float2* cs) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lph = a.lanes, l = lane & (lph - 1);
+                                           float2* cs, bool table) {
+  const int lane = threadIdx.x & 31, lph = a.lanes, l = lane & (lph - 1);
   const int per_warp = 32 / lph, slots = (kHnThreads / 32) * per_warp;
-  const int slot = warp * per_warp + lane / lph;
   const int D = a.dim, rot0 = p.rotate ? D - a.rope : D;
-  const T* x = static_cast<const T*>(p.x) + t * p.x_tok;
-  T* y = static_cast<T*>(p.y) + t * p.y_tok;
-  float w[NC][8];
-  bool first = true;
-  for (int hb = h0; hb < h1; hb += slots * U) {
-    Raw<T> raw[U][NC];
+  int h = h0 + (int)(threadIdx.x >> 5) * per_warp + lane / lph;
+  const T* x = static_cast<const T*>(p.x) + t * p.x_tok + h * p.x_head + l * 8;
+  T* y = static_cast<T*>(p.y) + t * p.y_tok + h * p.y_head + l * 8;
+  const int64_t x_step = slots * p.x_head, y_step = slots * p.y_head;
+  const float inv_d = 1.f / (float)D, eps = (float)a.eps;
+  const bool tiny_eps = a.eps < 1e-20;
+  uint64_t w[NC][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * slots + slot;
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = (c * lph + l) * 8 + 2 * i;
+      w[c][i] = p.weight != nullptr && d < D ? pair(__ldg(p.weight + d), __ldg(p.weight + d + 1)) : pair(1.f, 1.f);
+    }
+  Raw<T> next[U][NC];
+  auto fetch = [&](int at) {                             // heads at, at + slots, ...
+#pragma unroll
+    for (int u = 0; u < U; ++u, x += x_step) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int d0 = (c * lph + l) * 8;
-        raw[u][c].zero();
-        if (h < h1 && d0 < D) {
-          const T* px = x + h * p.x_head + d0;
-          if (p.vec) {
-            raw[u][c].load(px);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (d0 + e < D) raw[u][c].set(e, px[e]);
-          }
+        const int left = D - (c * lph + l) * 8;
+        next[u][c].zero();
+        if (at + u * slots < h1 && left > 0) {
+          if (kVec) next[u][c].load(x + c * lph * 8);
+          else next[u][c].load(x + c * lph * 8, left);
         }
       }
     }
-    if (first) {
-      first = false;
+  };
+  fetch(h);
+  for (int n = (h1 - h0 + slots * U - 1) / (slots * U); n > 0; --n) {      // the same count in every warp
+    Raw<T> raw[U][NC];
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = (c * lph + l) * 8 + e;
-          w[c][e] = p.weight != nullptr && d < D ? __ldg(p.weight + d) : 1.f;
-        }
-      if (p.rotate) {
-        const int64_t pos = a.positions[t];
-        for (int i = threadIdx.x; i < a.rope / 2; i += kHnThreads) {
-          float c = 1.f, s = 0.f;
-          rope_pair(c, s, a.theta[i], pos);            // rotating (1, 0) gives (cos, sin)
-          cs[i] = make_float2(c, s);
-        }
+      for (int c = 0; c < NC; ++c) raw[u][c] = next[u][c];
+    if (n > 1) fetch(h + U * slots);
+    if (table) {       // (the first pass of the block's first heads)
+      table = false;
+      const int64_t pos = a.positions != nullptr ? a.positions[t] : 0;
+      for (int i = threadIdx.x; i < a.rope / 2; i += kHnThreads) {
+        cs[i] = cos_sin((double)pos * a.theta[i]);
       }
       __syncthreads();
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * slots + slot;
-      float v[NC][8], ss = 0.f;
+    for (int u = 0; u < U; ++u, h += slots, y += y_step) {
+      uint64_t v[NC][4], s2 = 0;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[c][e] = raw[u][c].get(e);
-          ss = fmaf(v[c][e], v[c][e], ss);
+        for (int i = 0; i < 4; ++i) {
+          v[c][i] = raw[u][c].get(i);
+          s2 = fma2(v[c][i], v[c][i], s2);
         }
+      const float2 s = unpair(s2);
+      float ss = s.x + s.y;
       for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      // Squares beyond fp32's range (a sum that overflowed, or one that may
-      // have lost its small squares while eps does not cover them): the sum
-      // and the scale again, in fp64.
-      const bool wide = !(ss <= 3.0e38f) || (ss < 1e-30f && a.eps < 1e-20);
-      if (__any_sync(0xffffffffu, wide)) {
-        double s2 = 0.0;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s2 += (double)v[c][e] * v[c][e];
-        for (int o = lph >> 1; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-        const double r = 1.0 / sqrt(s2 / D + a.eps), r32 = (double)__frcp_rn(sqrtf(ss / (float)D + (float)a.eps));
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[c][e] = wide ? (float)(v[c][e] * r) : v[c][e] * (float)r32;
-      } else {
-        const float r = __frcp_rn(sqrtf(ss / (float)D + (float)a.eps));
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[c][e] *= r;
-      }
+      float r = __frcp_rn(sqrtf(fmaf(ss, inv_d, eps)));
+      const bool wide = !(ss <= 3.0e38f) || (tiny_eps && ss < 1e-30f);
+      if (__any_sync(0xffffffffu, wide)) wide_head<NC>(v, r, wide, lph, D, a.eps);
+      const uint64_t rr = pair(r, r);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int d0 = (c * lph + l) * 8;
-        if (h >= h1 || d0 >= D) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[c][e] *= w[c][e];
+        for (int i = 0; i < 4; ++i) v[c][i] = mul2(mul2(v[c][i], rr), w[c][i]);
         if (d0 + 8 > rot0) {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2)
-            if (d0 + e >= rot0 && d0 + e < D) {        // D and rot0 are even: a pair never straddles
-              const float2 q = cs[(d0 + e - rot0) >> 1];
-              const float x0 = v[c][e], x1 = v[c][e + 1];
-              v[c][e] = fmaf(x0, q.x, -(x1 * q.y));
-              v[c][e + 1] = fmaf(x0, q.y, x1 * q.x);
+          for (int i = 0; i < 4; ++i) {
+            const int d = d0 + 2 * i;                    // D and rot0 are even: a pair never straddles
+            if (d >= rot0 && d < D) {
+              const float2 q = cs[(d - rot0) >> 1], f = unpair(v[c][i]);
+              v[c][i] = pair(fmaf(f.x, q.x, -(f.y * q.y)), fmaf(f.x, q.y, f.y * q.x));
             }
+          }
         }
-        T* py = y + h * p.y_head + d0;
-        if (p.vec) {
-          put8(py, v[c]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (d0 + e < D) put1(py + e, v[c][e]);
-        }
+        if (h < h1 && d0 < D) Raw<T>::store(y + c * lph * 8, v[c], kVec ? -1 : D - d0);
       }
     }
   }
 }
 
 template <int NC>
-__global__ void __launch_bounds__(kHnThreads) head_norm_kernel(const __grid_constant__ HeadNormArgs a) {
+__device__ __forceinline__ void norm_part(const HeadNormArgs& a, const HeadNormPart& p, int64_t t, int h0, int h1,
+                                          float2* cs, bool table) {
+  // heads in flight a warp: as many as the registers hold twice
+  constexpr int U = NC == 1 ? 2 : 1;
+  if (p.f32) {
+    if (p.vec) norm_heads<float, NC, U, true>(a, p, t, h0, h1, cs, table);
+    else norm_heads<float, NC, 1, false>(a, p, t, h0, h1, cs, table);
+  } else {
+    if (p.vec) norm_heads<uint16_t, NC, NC == 4 ? 1 : 2, true>(a, p, t, h0, h1, cs, table);
+    else norm_heads<uint16_t, NC, 1, false>(a, p, t, h0, h1, cs, table);
+  }
+}
+
+template <int NC>
+__global__ void __launch_bounds__(kHnThreads, NC == 4 ? 3 : 4) head_norm_kernel(const __grid_constant__ HeadNormArgs a) {
   __shared__ float2 cs[kHnMaxDim / 2];
-  const int per_tok = a.part[0].blocks + a.part[1].blocks;
-  const int64_t t = blockIdx.x / per_tok;
-  int b = blockIdx.x % per_tok;
-  const int which = b >= a.part[0].blocks ? 1 : 0;
-  const HeadNormPart& p = a.part[which];
-  if (which) b -= a.part[0].blocks;
-  const int h0 = b * p.block_heads, h1 = min(p.heads, h0 + p.block_heads);
-  constexpr int U = NC == 1 ? 4 : NC == 2 ? 2 : 1;
-  if (p.f32) norm_heads<float, NC, U>(a, p, t, h0, h1, cs);
-  else norm_heads<uint16_t, NC, U>(a, p, t, h0, h1, cs);
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
+  const int64_t t = blockIdx.x / a.blocks;
+  const int b = blockIdx.x % a.blocks;
+  const HeadNormPart &q = a.part[0], &k = a.part[1];
+  const int qb = b - q.block0, kb = b - k.block0;
+  const bool has_q = qb >= 0 && qb < q.blocks, has_k = kb >= 0 && kb < k.blocks;
+  const bool table = (has_q && q.rotate) || (has_k && k.rotate);
+  if (has_q) norm_part<NC>(a, q, t, qb * q.block_heads, min(q.heads, (qb + 1) * q.block_heads), cs, table);
+  if (has_k) norm_part<NC>(a, k, t, kb * k.block_heads, min(k.heads, (kb + 1) * k.block_heads), cs, table && !has_q);
 }
 
 }  // namespace
@@ -213,29 +292,40 @@ cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st) {
   while (a.lanes < 32 && a.lanes < steps) a.lanes *= 2;
   const int nc = (steps + 31) / 32;
   const int slots = (kHnThreads / 32) * (32 / a.lanes);
-  int64_t per_tok = 0;
+  // A token's heads in one block once the tokens alone give every SM 8 blocks
+  // (the sines are computed once a token, the keys follow the queries); for
+  // fewer tokens the heads are spread over blocks of at least one pass, the
+  // keys in blocks of their own.
+  const int64_t want = (8LL * sms + a.n_tok - 1) / a.n_tok;
+  int64_t blocks = 0;
   for (HeadNormPart& p : a.part) {
-    if (p.heads == 0) { p.blocks = 0; p.block_heads = 1; continue; }
-    const int esz = p.f32 ? 4 : 2, al = 16 / esz;
+    if (p.heads == 0) { p.blocks = p.block0 = 0; p.block_heads = 1; continue; }
+    const int al = p.f32 ? 4 : 8;
     p.vec = a.dim % 8 == 0 && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && reinterpret_cast<uintptr_t>(p.y) % 16 == 0 &&
             p.x_tok % al == 0 && p.x_head % al == 0 && p.y_tok % al == 0 && p.y_head % al == 0;
-    // A token's heads in one block once the tokens alone give every SM 8
-    // blocks; for fewer tokens the heads are spread over blocks of one pass.
-    const int64_t want = (8LL * sms + a.n_tok - 1) / a.n_tok;
     int64_t bh = (p.heads + want - 1) / want;
     bh = (bh + slots - 1) / slots * slots;
     p.block_heads = (int)bh;
     p.blocks = (int)((p.heads + bh - 1) / bh);
-    per_tok += p.blocks;
+    p.block0 = want == 1 ? 0 : (int)blocks;
+    blocks = std::max<int64_t>(blocks, p.block0 + p.blocks);
   }
-  const int64_t grid = per_tok * a.n_tok;
+  a.blocks = (int)blocks;
+  const int64_t grid = blocks * a.n_tok;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   if (grid == 0) return cudaSuccess;
-  const dim3 g((unsigned)grid);
-  if (nc == 1) head_norm_kernel<1><<<g, kHnThreads, 0, st>>>(a);
-  else if (nc == 2) head_norm_kernel<2><<<g, kHnThreads, 0, st>>>(a);
-  else head_norm_kernel<4><<<g, kHnThreads, 0, st>>>(a);
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(kHnThreads);
+  lc.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&lc, nc == 1 ? head_norm_kernel<1> : nc == 2 ? head_norm_kernel<2> : head_norm_kernel<4>, a);
   note_launch();
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

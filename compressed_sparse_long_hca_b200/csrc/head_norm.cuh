@@ -10,7 +10,7 @@ struct HeadNormPart {                  // the query heads, or the key heads
   const float* weight;                 // [dim], or null (ones)
   int64_t x_tok, x_head, y_tok, y_head;   // strides in elements
   int heads, f32, rotate;
-  int vec, block_heads, blocks;        // set by the launch
+  int vec, block_heads, block0, blocks;   // set by the launch: its blocks of a token are block0, ..., block_heads heads each
 };
 
 struct HeadNormArgs {
@@ -19,7 +19,7 @@ struct HeadNormArgs {
   const double* theta;                 // [rope / 2]
   double eps;
   int dim, rope;
-  int lanes;                           // lanes of a head (set by the launch)
+  int lanes, blocks;                   // lanes of a head, blocks of a token (set by the launch)
   HeadNormPart part[2];
 };
 
