@@ -100,7 +100,7 @@ struct Cfg {
   static constexpr uint32_t kWsfBase = 2 * NT, kXsfBase = kWsfBase + 4 * kSfRing;
   static constexpr uint32_t kColsNeeded = kXsfBase + 4 * kChunks * kXsfRing;
   static constexpr uint32_t kTmemCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 256 + 128;
+  static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 256 + 128;   // ring, barriers, alignment
   static_assert(kColsNeeded <= 512 && kTmemCols * kPerSm <= 512, "TMEM");
   static_assert(kStages >= 3 && kStages <= 8 && kBatch <= kStages, "stages");
   static_assert(!FUSE || NT == 16, "a quantising thread takes one unit of a block");
@@ -248,8 +248,7 @@ __global__ void __launch_bounds__(256) fp8_quant_x_kernel(const uint16_t* x, int
   }
 }
 
-// Warp 0 issues the bulk copies, warp 1 the scale copies and MMAs (one elected
-// lane each), the next 4 or 8 read the accumulators (a thread = one output
+// Warp 0 issues the bulk copies, warp 1 the scale copies and MMAs, the next 4 or 8 read the accumulators (a thread = one output
 // feature, its columns = tokens), the last 4 (FUSE) quantise the tokens.
 template <int NT, bool FUSE>
 __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm)
@@ -265,7 +264,10 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile uint32_t* issued_slot = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);   // stages the producer filled
+  // (broadcast: the role and the TMEM base are then known to be warp-uniform,
+  // and the MMAs' operands need no move between register files)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr uint64_t kLimit = 1000000000ull;
   constexpr int kXOff = kWTileBytes, kWsfOff = kXOff + NT * kKBlk, kXsfOff = kWsfOff + kSfBytes;   // in a stage
 
@@ -279,12 +281,13 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
     for (int x = 0; x < 2; ++x) { tc::mbar_init(&acc_full[x], 1); tc::mbar_init(&acc_empty[x], C::kEpi); }
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
+    *issued_slot = 0;
     tc::fence_mbar_init();
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int rows_per_group = a.n_out / a.groups;
   const int xb = a.tile_n * kKBlk;                      // bytes of one packed activation block
   const int n_sfb = (a.tile_n + 127) / 128;             // its scale chunks
@@ -298,99 +301,111 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
   const int k1 = a.spread ? part_begin(a.k_blocks, a.splits, part + 1) : a.k_blocks;
   const int q0 = part, q1 = a.spread ? part + 1 : a.splits;
   bool ok = true;
-  uint32_t issued = 0;                                  // producer: stages filled
   if (warp == 0) {
-    // ---- producer.  The weight does not depend on the kernels ahead (the
-    //      packing ends with a kernel of its own): its first stages are
-    //      issued before waiting for them.
-    bool waited = FUSE;
-    uint32_t pre = 0;                                   // stages whose weight copies are already issued
-    auto put_w = [&](uint32_t x, int rt, int kb, bool sf) {
-      uint8_t* st = sm + (size_t)(x % S) * C::kStageBytes;
-      const uint32_t xbytes = FUSE ? 0u : (uint32_t)(xb + (sf ? kSfBytes * n_sfb : 0));
-      tc::mbar_arrive_expect_tx(&full[x % S], (uint32_t)(kWTileBytes + (sf ? kSfBytes : 0)) + xbytes);
-      tc::bulk_g2s(st, a.w + ((int64_t)rt * a.k_blocks + kb) * kWTileBytes, kWTileBytes, &full[x % S]);
-      if (sf) tc::bulk_g2s(st + kWsfOff, a.wsf + ((int64_t)rt * a.sup + (kb >> 2)) * kSfBytes, kSfBytes, &full[x % S]);
-    };
-    auto put_x = [&](uint32_t x, int rt, int tt, int kb, bool sf) {
-      uint8_t* st = sm + (size_t)(x % S) * C::kStageBytes;
-      const int64_t grp = (rt * kRowTile) / rows_per_group;
-      tc::bulk_g2s(st + kXOff, a.xp + ((grp * a.k_blocks + kb) * a.tok_tiles + tt) * xb, (uint32_t)xb, &full[x % S]);
-      if (sf)
-        tc::bulk_g2s(st + kXsfOff, a.xsf + ((grp * a.sup + (kb >> 2)) * a.tok_tiles + tt) * n_sfb * kSfBytes,
-                     (uint32_t)(kSfBytes * n_sfb), &full[x % S]);
-    };
-    if (!FUSE) {
-      pre = (uint32_t)(k1 - k0 < S ? k1 - k0 : S);
-      if (tc::elect_one())
+    // ---- producer (one thread).  The weight does not depend on the kernels
+    //      ahead (the packing ends with a kernel of its own): its first stages
+    //      are issued before waiting for them.
+    if (tc::elect_one()) {
+      auto put_w = [&](uint32_t st, int rt, int kb, bool sf) {
+        uint8_t* at = sm + st * C::kStageBytes;
+        const uint32_t xbytes = FUSE ? 0u : (uint32_t)(xb + (sf ? kSfBytes * n_sfb : 0));
+        tc::mbar_arrive_expect_tx(&full[st], (uint32_t)(kWTileBytes + (sf ? kSfBytes : 0)) + xbytes);
+        tc::bulk_g2s(at, a.w + ((int64_t)rt * a.k_blocks + kb) * kWTileBytes, kWTileBytes, &full[st]);
+        if (sf) tc::bulk_g2s(at + kWsfOff, a.wsf + ((int64_t)rt * a.sup + (kb >> 2)) * kSfBytes, kSfBytes, &full[st]);
+      };
+      uint32_t pre = 0;                                 // stages whose weight copies are already issued
+      if (!FUSE) {
+        pre = (uint32_t)(k1 - k0 < S ? k1 - k0 : S);
         for (uint32_t x = 0; x < pre; ++x) put_w(x, it0 / a.tok_tiles, k0 + (int)x, x == 0 || ((k0 + (int)x) & 3) == 0);
-      __syncwarp();
-    }
-    for (int it = it0; it < a.tiles && ok; it += it_step) {
-      const int rt = it / a.tok_tiles, tt = it % a.tok_tiles;
-      if (!waited) { tc::griddep_wait(); waited = true; }
-      for (int kb = k0; kb < k1; ++kb) {
-        const uint32_t x = issued;
-        if (x >= (uint32_t)S) ok = tc::mbar_wait(&empty[x % S], ((x / S) - 1) & 1, kLimit) && !*abort_flag;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const bool sf = kb == k0 || (kb & 3) == 0;
-        if (tc::elect_one()) {
-          if (x >= pre) put_w(x, rt, kb, sf);
-          if (!FUSE) put_x(x, rt, tt, kb, sf);
-        }
-        __syncwarp();
-        issued = x + 1;
+        tc::griddep_wait();
       }
-    }
-    if (!ok) *abort_flag = 1;
-    if (issued < pre) {       // (an abort in between) the stages whose weight copies are in flight without their tokens
-      if (tc::elect_one())
-        for (uint32_t x = issued; x < pre; ++x) tc::mbar_wait(&full[x % S], 0, 1000ull);
-      __syncwarp();
-    }
-  } else if (warp == 1) {
-    // ---- scale copies and MMAs
-    uint32_t x = 0, u = 0, nsf = 0;                     // stage, accumulator and scale-buffer counters
-    for (int it = it0; it < a.tiles && ok; it += it_step) {
-      for (int q = q0; q < q1 && ok; ++q, ++u) {
-        const int b0 = part_begin(a.k_blocks, a.splits, q), b1 = part_begin(a.k_blocks, a.splits, q + 1);
-        const uint32_t acc = tmem + (u & 1) * NT;
-        if (u >= 2) ok = tc::mbar_wait(&acc_empty[u & 1], ((u >> 1) - 1) & 1, kLimit);
-        for (int kb = b0; kb < b1; ++kb, ++x) {
-          ok = ok && tc::mbar_wait(&full[x % S], (x / S) & 1, kLimit) && !*abort_flag;
-          ok = __all_sync(0xffffffffu, ok);
+      uint32_t x = 0, st = 0, ph = 1;                   // stages filled; the stage and its last release's phase
+      for (int it = it0; it < a.tiles && ok; it += it_step) {
+        const int rt = it / a.tok_tiles, tt = it % a.tok_tiles;
+        const int64_t grp = (rt * kRowTile) / rows_per_group;
+        const uint8_t* xp = a.xp + (grp * a.k_blocks * a.tok_tiles + tt) * xb;
+        const uint8_t* xsf = a.xsf + (grp * a.sup * a.tok_tiles + tt) * n_sfb * kSfBytes;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (x >= (uint32_t)S) ok = tc::mbar_wait(&empty[st], ph, kLimit);
           if (!ok) break;
-          tc::tc_fence_after();
           const bool sf = kb == k0 || (kb & 3) == 0;
-          if (sf) ++nsf;
-          // A scale buffer of four blocks is rewritten four loads after its
-          // own: by then the MMAs that read it are complete, for the stage
-          // just waited for was free (S <= 8 blocks back), or the accumulator
-          // two tiles back was.  The tokens' buffers of one block (FUSE) are
-          // rewritten 8 >= S blocks later.
-          const uint32_t wsf = tmem + C::kWsfBase + ((nsf - 1) % kSfRing) * 4;
-          const uint32_t xsf = tmem + C::kXsfBase + (FUSE ? x % C::kXsfRing : (nsf - 1) % kSfRing) * 4 * C::kChunks;
-          const uint32_t wb = tc::smem_u32(sm + (size_t)(x % S) * C::kStageBytes), xbase = wb + kXOff;
-          if (tc::elect_one()) {
-            if (sf) tc::tmem_cp_32x128b_x4(wsf, tc::smem_desc(wb + kWsfOff, 128, 128));
-            if (FUSE || sf)
-              for (int ch = 0; ch < n_sfb; ++ch)
-                tc::tmem_cp_32x128b_x4(xsf + 4 * ch, tc::smem_desc(wb + kXsfOff + kSfBytes * ch, 128, 128));
-            const uint32_t id = kb & 3, xid = FUSE ? 0u : id;
-            const uint32_t idesc = tc::idesc_mxf8(kRowTile, a.tile_n, id, xid);
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              tc::mma_mxf8(acc, tc::smem_desc(wb + m * 256, 128, 1024), tc::smem_desc(xbase + m * 256, 128, 1024), idesc,
-                           wsf | (id << 30), xsf | (xid << 30), (kb > b0 || m > 0) ? 1u : 0u);
-            tc::mma_commit(&empty[x % S]);
-            if (kb == b1 - 1) tc::mma_commit(&acc_full[u & 1]);
+          if (x >= pre) put_w(st, rt, kb, sf);
+          if (!FUSE) {
+            uint8_t* at = sm + st * C::kStageBytes;
+            tc::bulk_g2s(at + kXOff, xp + (int64_t)kb * a.tok_tiles * xb, (uint32_t)xb, &full[st]);
+            if (sf)
+              tc::bulk_g2s(at + kXsfOff, xsf + (int64_t)(kb >> 2) * a.tok_tiles * n_sfb * kSfBytes,
+                           (uint32_t)(kSfBytes * n_sfb), &full[st]);
           }
-          __syncwarp();
+          ++x;
+          if (++st == S) { st = 0; ph ^= 1; }
         }
       }
+      *issued_slot = x;
+      if (!ok) *abort_flag = 1;
+      for (; x < pre; ++x) tc::mbar_wait(&full[x], 0, 1000ull);   // (an abort before) weight copies without their tokens
     }
-    if (!ok) *abort_flag = 1;
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- scale copies and MMAs (one thread).  Issuing a block's four MMAs
+    //      bounds narrow tiles: 680 cycles a block with descriptors built from
+    //      their fields in a warp-wide loop, 330 with one thread's loop over
+    //      uniform values, where base values plus multiples of the stage and
+    //      block are counted along (four MMAs themselves: 128 cycles at 64
+    //      tokens, 448 at 224).
+    if (tc::elect_one()) {
+      const uint32_t desc_hi = tc::smem_desc_hi(1024), sf_hi = tc::smem_desc_hi(128);
+      const uint32_t lo0 = tc::smem_desc_lo(tc::smem_u32(sm), 128);
+      const uint32_t idesc0 = tc::idesc_mxf8(kRowTile, a.tile_n, 0, 0);
+      constexpr uint32_t kIdStep = (1u << 29) | (FUSE ? 0u : 1u << 4);   // the scale byte of the next block
+      uint32_t st = 0, ph = 0;                          // stage and its phase
+      uint32_t u = 0;                                   // accumulators used
+      uint32_t wr = kSfRing - 1, xr = FUSE ? 0 : kSfRing - 1;   // scale buffers in use
+      for (int it = it0; it < a.tiles && ok; it += it_step) {
+        int kb = k0;
+        for (int q = q0; q < q1 && ok; ++q, ++u) {
+          const int b1 = part_begin(a.k_blocks, a.splits, q + 1);
+          const uint32_t acc = tmem + (u & 1) * NT;
+          if (u >= 2) ok = tc::mbar_wait(&acc_empty[u & 1], ((u >> 1) - 1) & 1, kLimit);
+          for (uint32_t more = 0; kb < b1; ++kb, more = 1) {
+            ok = ok && tc::mbar_wait(&full[st], ph, kLimit);
+            if (!ok) break;
+            tc::tc_fence_after();
+            // A scale buffer of four blocks is rewritten four loads after its
+            // own: by then the MMAs that read it are complete, for the stage
+            // just waited for was free (S <= 8 blocks back), or the
+            // accumulator two tiles back was.  The tokens' buffers of one
+            // block (FUSE) are rewritten 8 >= S blocks later.
+            const bool sf = kb == k0 || (kb & 3) == 0;
+            if (sf) {
+              wr = (wr + 1) & (kSfRing - 1);
+              if (!FUSE) xr = wr;
+            }
+            const uint32_t id = kb & 3, lo = lo0 + st * (C::kStageBytes / 16);
+            const uint32_t wsf = tmem + C::kWsfBase + wr * 4, xsf = tmem + C::kXsfBase + xr * 4 * C::kChunks;
+            const uint32_t wsf_id = wsf | (id << 30), xsf_id = FUSE ? xsf : xsf | (id << 30);
+            const uint32_t idesc = idesc0 + id * kIdStep;
+            if (sf) tc::tmem_cp_32x128b_x4(wsf, tc::desc64(lo + kWsfOff / 16, sf_hi));
+            if (FUSE || sf) {
+#pragma unroll
+              for (int ch = 0; ch < C::kChunks; ++ch)
+                if (ch < n_sfb) tc::tmem_cp_32x128b_x4(xsf + 4 * ch, tc::desc64(lo + (kXsfOff + kSfBytes * ch) / 16, sf_hi));
+            }
+            tc::mma_mxf8(acc, tc::desc64(lo, desc_hi), tc::desc64(lo + kXOff / 16, desc_hi), idesc, wsf_id, xsf_id, more);
+#pragma unroll
+            for (int m = 1; m < 4; ++m)
+              tc::mma_mxf8(acc, tc::desc64(lo + m * 16, desc_hi), tc::desc64(lo + kXOff / 16 + m * 16, desc_hi), idesc, wsf_id,
+                           xsf_id, 1u);
+            tc::mma_commit(&empty[st]);
+            if (kb + 1 == b1) tc::mma_commit(&acc_full[u & 1]);
+            if (FUSE) xr = (xr + 1) & (C::kXsfRing - 1);
+            if (++st == S) { st = 0; ph ^= 1; }
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
   } else if (FUSE && warp >= 2 + C::kEpi / 32) {
     // ---- token quantiser: the blocks of this CTA's tiles, kBatch at a time: all
     //      their loads in flight together, one proxy fence for all (a fence
@@ -540,6 +555,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
   if (*abort_flag && tid == 0) {
     if (atomicCAS(&g_fp8_err[0], 0, (int32_t)kErrTimeout) == 0) g_fp8_err[1] = (int32_t)blockIdx.x;
     // let the copies already issued land before the shared memory goes away
+    const uint32_t issued = *issued_slot;
     for (uint32_t x = issued > (uint32_t)S ? issued - S : 0; x < issued; ++x)
       tc::mbar_wait(&full[x % S], (x / S) & 1, 200000000ull);
   }

@@ -149,6 +149,14 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
   return d;                 // base offset 0, swizzle none
 }
 
+// The same descriptor by halves: `lo` moves with the address (+ bytes / 16),
+// `hi` is constant.
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFF) | ((lbo >> 4) & 0x3FFF) << 16;
+}
+__device__ __forceinline__ uint32_t smem_desc_hi(uint32_t sbo) { return ((sbo >> 4) & 0x3FFF) | 1u << 14; }
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
+
 // Instruction descriptor of kind::mxf4 (E2M1 x E2M1, E8M0 scales per 32,
 // fp32 accumulate), both operands K-major.
 __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, uint32_t a_sf_id, uint32_t b_sf_id) {
