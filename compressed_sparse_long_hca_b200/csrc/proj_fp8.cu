@@ -43,8 +43,7 @@
 
 #include <algorithm>
 
-#include "common.cuh"
-#include "gemm_out.cuh"
+#include "proj_fp8.cuh"
 #include "tc.cuh"
 
 namespace csa {
@@ -55,15 +54,6 @@ namespace cg = cooperative_groups;
 __device__ int32_t g_fp8_err[2];
 
 namespace {
-
-constexpr int kRowTile = 128;                 // output features per tile (MMA M)
-constexpr int kKBlk = 128;                    // K per stage: one scale block
-constexpr int kWTileBytes = kRowTile * kKBlk; // 16 KB
-constexpr int kSfBytes = 512;                 // scales of 128 rows x 4 blocks, tcgen05.cp order
-constexpr int kSfRing = 4;                    // scale buffers in TMEM
-constexpr int kMinPartBlocks = 4;             // K blocks of the smallest part
-constexpr int kMaxParts = 8;                  // parts of a weight: CTAs of the largest portable cluster
-constexpr int kFuseTokens = 16;               // most tokens that the product quantises itself
 
 struct Fp8Args {
   const uint8_t* w;       // packed weight: tiles [row_tiles][k_blocks][16 KB]
@@ -106,45 +96,6 @@ struct Cfg {
   static_assert(!FUSE || NT == 16, "a quantising thread takes one unit of a block");
   static_assert(kRowTile * NT * 4 <= kStages * kStageBytes, "a part's sums fit in the ring");
 };
-
-// The first K block of part p (parts differ by at most one block).
-__host__ __device__ inline int part_begin(int k_blocks, int splits, int p) {
-  return (int)((int64_t)k_blocks * p / splits);
-}
-
-// Where an output feature goes: element (token t) at y + t * rows.
-struct OutRow {
-  void* y;
-  int64_t rows;
-  bool bf16;
-  __device__ __forceinline__ void store(int t, float v) const {
-    if (bf16) static_cast<uint16_t*>(y)[t * rows] = bf16_rn(v);
-    else static_cast<float*>(y)[t * rows] = v;
-  }
-  // Tokens t .. t + 15, the first n of them.
-  __device__ __forceinline__ void store16(int t, int n, const float* v) const {
-    if (bf16) {
-      uint16_t* p = static_cast<uint16_t*>(y) + t * rows;
-#pragma unroll
-      for (int e = 0; e < 16; ++e, p += rows)
-        if (e < n) *p = bf16_rn(v[e]);
-    } else {
-      float* p = static_cast<float*>(y) + t * rows;
-#pragma unroll
-      for (int e = 0; e < 16; ++e, p += rows)
-        if (e < n) *p = v[e];
-    }
-  }
-};
-
-__device__ __forceinline__ OutRow out_row(const GemmOut& out, int o) {
-  int sg = 0;
-  while (sg + 1 < out.n_seg && o >= out.seg_end[sg]) ++sg;
-  const int r0 = sg > 0 ? out.seg_end[sg - 1] : 0;
-  const bool bf16 = (out.bf16_mask >> sg) & 1u;
-  char* y = static_cast<char*>(out.y[sg]);
-  return OutRow{y + (int64_t)(o - r0) * (bf16 ? 2 : 4), out.seg_end[sg] - r0, bf16};
-}
 
 }  // namespace
 
@@ -214,37 +165,40 @@ __device__ __forceinline__ uint32_t quant_unit(const Unit& u, uint4& codes) {
   return (uint32_t)(finite ? e + 127 : 255);
 }
 
-// Offset of row r's 16-byte column c in a block of rows x 128 codes (no-swizzle
-// K-major core matrices), and of row r's scale word in a 512-byte chunk.
-__device__ __forceinline__ int code_off(int r, int c) { return (r >> 3) * 1024 + c * 128 + (r & 7) * 16; }
-__device__ __forceinline__ int scale_off(int r) { return 16 * (r & 31) + 4 * ((r >> 5) & 3); }
-
-// Quantise X (BF16 [n_tok][groups * kg]) into the B operand's blocks, 16
-// values a thread.  Rows beyond n_tok of the last tile and columns beyond kg
-// of the last block are zero; scales nothing reads are left as they are.
+// Quantise X (BF16 [n_tok][groups * kg]) into the B operand's blocks: a thread
+// block takes 32 rows (8 threads each) of the K blocks blockIdx.y, blockIdx.y +
+// gridDim.y, ... of a group, two at a time.  Rows beyond n_tok of the last tile
+// and columns beyond kg of the last block are zero; scales nothing reads are
+// left as they are.
 __global__ void __launch_bounds__(256) fp8_quant_x_kernel(const uint16_t* x, int n_tok, int kg, int64_t row_len,
                                                           int k_blocks, int sup, int tok_tiles, int tile_n, int chunks,
                                                           bool aligned, uint8_t* xp, uint8_t* xsf) {
   tc::griddep_launch_dependents();
   tc::griddep_wait();
-  const int g = blockIdx.y;
-  x += (int64_t)g * kg;
-  xp += (int64_t)g * k_blocks * tok_tiles * tile_n * kKBlk;
-  xsf += (int64_t)g * sup * tok_tiles * chunks * kSfBytes;
-  const int n_pad = tok_tiles * tile_n;                  // a multiple of 4
-  const int64_t total = (int64_t)k_blocks * n_pad * 8;
-  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < total; u += (int64_t)gridDim.x * blockDim.x) {
-    // 32 consecutive units: 4 rows, the row in lane bits 0-1, the column in bits 2-4
-    const int c = (int)((u >> 2) & 7);
-    const int64_t row = (u >> 5) * 4 + (u & 3);
-    const int t = (int)(row % n_pad), b = (int)(row / n_pad);
-    const int k0 = b * kKBlk + c * 16;
-    const Unit v = load_unit(x + (int64_t)t * row_len + k0, t < n_tok ? kg - k0 : 0, aligned);
-    uint4 codes;
-    const uint32_t sf = quant_unit(v, codes);
-    const int j = t / tile_n, r = t % tile_n;
-    *reinterpret_cast<uint4*>(xp + ((int64_t)b * tok_tiles + j) * tile_n * kKBlk + code_off(r, c)) = codes;
-    if (c == 0) xsf[(((int64_t)(b >> 2) * tok_tiles + j) * chunks + (r >> 7)) * kSfBytes + scale_off(r) + (b & 3)] = (uint8_t)sf;
+  const int g = blockIdx.z, n_pad = tok_tiles * tile_n;  // a multiple of 16
+  // a warp: 4 rows, the row in lane bits 0-1, the column in bits 2-4
+  const int c = (threadIdx.x >> 2) & 7, t = blockIdx.x * 32 + (threadIdx.x >> 5) * 4 + (threadIdx.x & 3);
+  if (t >= n_pad) return;                                // (whole warps)
+  const int j = t / tile_n, r = t - j * tile_n;
+  const uint16_t* row = x + (t < n_tok ? (int64_t)t * row_len : 0) + (int64_t)g * kg + c * 16;
+  const int cols = t < n_tok ? kg - c * 16 : 0;
+  const int64_t block = (int64_t)tok_tiles * tile_n * kKBlk;
+  uint8_t* xd = xp + (int64_t)g * k_blocks * block + (int64_t)j * tile_n * kKBlk + code_off(r, c);
+  uint8_t* sd = xsf + ((int64_t)g * sup * tok_tiles + j) * chunks * kSfBytes + (r >> 7) * kSfBytes + scale_off(r);
+  const int64_t sf_step = (int64_t)tok_tiles * chunks * kSfBytes;
+  for (int b0 = blockIdx.y; b0 < k_blocks; b0 += 2 * gridDim.y) {
+    const int b1 = b0 + gridDim.y;
+    const bool two = b1 < k_blocks;
+    const Unit u0 = load_unit(row + (int64_t)b0 * kKBlk, cols - b0 * kKBlk, aligned);
+    const Unit u1 = load_unit(row + (two ? (int64_t)b1 * kKBlk : 0), two ? cols - b1 * kKBlk : 0, aligned);
+    uint4 q0, q1;
+    const uint32_t s0 = quant_unit(u0, q0), s1 = quant_unit(u1, q1);
+    *reinterpret_cast<uint4*>(xd + b0 * block) = q0;
+    if (c == 0) sd[(b0 >> 2) * sf_step + (b0 & 3)] = (uint8_t)s0;
+    if (two) {
+      *reinterpret_cast<uint4*>(xd + b1 * block) = q1;
+      if (c == 0) sd[(b1 >> 2) * sf_step + (b1 & 3)] = (uint8_t)s1;
+    }
   }
 }
 
@@ -306,44 +260,63 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
     //      ahead (the packing ends with a kernel of its own): its first stages
     //      are issued before waiting for them.
     if (tc::elect_one()) {
-      auto put_w = [&](uint32_t st, int rt, int kb, bool sf) {
-        uint8_t* at = sm + st * C::kStageBytes;
-        const uint32_t xbytes = FUSE ? 0u : (uint32_t)(xb + (sf ? kSfBytes * n_sfb : 0));
-        tc::mbar_arrive_expect_tx(&full[st], (uint32_t)(kWTileBytes + (sf ? kSfBytes : 0)) + xbytes);
-        tc::bulk_g2s(at, a.w + ((int64_t)rt * a.k_blocks + kb) * kWTileBytes, kWTileBytes, &full[st]);
-        if (sf) tc::bulk_g2s(at + kWsfOff, a.wsf + ((int64_t)rt * a.sup + (kb >> 2)) * kSfBytes, kSfBytes, &full[st]);
-      };
-      uint32_t pre = 0;                                 // stages whose weight copies are already issued
-      if (!FUSE) {
-        pre = (uint32_t)(k1 - k0 < S ? k1 - k0 : S);
-        for (uint32_t x = 0; x < pre; ++x) put_w(x, it0 / a.tok_tiles, k0 + (int)x, x == 0 || ((k0 + (int)x) & 3) == 0);
-        tc::griddep_wait();
-      }
+      // (every instruction between two blocks counts: addresses run along)
+      const uint32_t sm0 = tc::smem_u32(sm), full0 = tc::smem_u32(full);
+      const uint32_t x_sf = (uint32_t)(kSfBytes * n_sfb);
+      const uint32_t bytes = (uint32_t)(kWTileBytes + (FUSE ? 0 : xb)), sf_bytes = kSfBytes + (FUSE ? 0u : x_sf);
+      const int64_t xp_step = (int64_t)a.tok_tiles * xb, xsf_step = (int64_t)a.tok_tiles * x_sf;
       uint32_t x = 0, st = 0, ph = 1;                   // stages filled; the stage and its last release's phase
+      const int pre = k1 - k0 < S ? k1 - k0 : S;        // blocks whose weight copies are issued ahead
+      {
+        const int rt = it0 / a.tok_tiles;
+        const uint8_t* w = a.w + ((int64_t)rt * a.k_blocks + k0) * kWTileBytes;
+        const uint8_t* wsf = a.wsf + ((int64_t)rt * a.sup + (k0 >> 2)) * kSfBytes;
+        for (int i = 0; i < pre; ++i, w += kWTileBytes) {
+          const uint32_t at = sm0 + i * C::kStageBytes, bar = full0 + i * 8;
+          const bool sf = i == 0 || ((k0 + i) & 3) == 0;
+          tc::mbar_expect_tx_at(bar, bytes + (sf ? sf_bytes : 0u));
+          tc::bulk_g2s_at(at, w, kWTileBytes, bar);
+          if (sf) {
+            tc::bulk_g2s_at(at + kWsfOff, wsf, kSfBytes, bar);
+            wsf += kSfBytes;
+          }
+        }
+      }
+      if (!FUSE) tc::griddep_wait();
       for (int it = it0; it < a.tiles && ok; it += it_step) {
         const int rt = it / a.tok_tiles, tt = it % a.tok_tiles;
         const int64_t grp = (rt * kRowTile) / rows_per_group;
-        const uint8_t* xp = a.xp + (grp * a.k_blocks * a.tok_tiles + tt) * xb;
-        const uint8_t* xsf = a.xsf + (grp * a.sup * a.tok_tiles + tt) * n_sfb * kSfBytes;
+        const uint8_t* w = a.w + ((int64_t)rt * a.k_blocks + k0) * kWTileBytes;
+        const uint8_t* wsf = a.wsf + ((int64_t)rt * a.sup + (k0 >> 2)) * kSfBytes;
+        const uint8_t* xp = a.xp + ((grp * a.k_blocks + k0) * a.tok_tiles + tt) * xb;
+        const uint8_t* xsf = a.xsf + ((grp * a.sup + (k0 >> 2)) * a.tok_tiles + tt) * x_sf;
         for (int kb = k0; kb < k1; ++kb) {
-          if (x >= (uint32_t)S) ok = tc::mbar_wait(&empty[st], ph, kLimit);
+          ok = tc::mbar_wait(&empty[st], ph, kLimit);   // (a fresh barrier's wait for phase 1 passes)
           if (!ok) break;
-          const bool sf = kb == k0 || (kb & 3) == 0;
-          if (x >= pre) put_w(st, rt, kb, sf);
-          if (!FUSE) {
-            uint8_t* at = sm + st * C::kStageBytes;
-            tc::bulk_g2s(at + kXOff, xp + (int64_t)kb * a.tok_tiles * xb, (uint32_t)xb, &full[st]);
-            if (sf)
-              tc::bulk_g2s(at + kXsfOff, xsf + (int64_t)(kb >> 2) * a.tok_tiles * n_sfb * kSfBytes,
-                           (uint32_t)(kSfBytes * n_sfb), &full[st]);
+          const uint32_t at = sm0 + st * C::kStageBytes, bar = full0 + st * 8;
+          const bool ahead = (int)x < pre;              // its weight copies are issued
+          if (kb == k0 || (kb & 3) == 0) {
+            if (!ahead) {
+              tc::mbar_expect_tx_at(bar, bytes + sf_bytes);
+              tc::bulk_g2s_at(at + kWsfOff, wsf, kSfBytes, bar);
+            }
+            if (!FUSE) tc::bulk_g2s_at(at + kXsfOff, xsf, x_sf, bar);
+            wsf += kSfBytes;
+            xsf += xsf_step;
+          } else if (!ahead) {
+            tc::mbar_expect_tx_at(bar, bytes);
           }
+          if (!ahead) tc::bulk_g2s_at(at, w, kWTileBytes, bar);
+          if (!FUSE) tc::bulk_g2s_at(at + kXOff, xp, (uint32_t)xb, bar);
+          w += kWTileBytes;
+          xp += xp_step;
           ++x;
           if (++st == S) { st = 0; ph ^= 1; }
         }
       }
       *issued_slot = x;
       if (!ok) *abort_flag = 1;
-      for (; x < pre; ++x) tc::mbar_wait(&full[x], 0, 1000ull);   // (an abort before) weight copies without their tokens
+      for (; (int)x < pre; ++x) tc::mbar_wait(&full[x], 0, 1000ull);   // (an abort before) weight copies without their tokens
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -602,6 +575,21 @@ __global__ void __launch_bounds__(256) fp8_pack_w_kernel(const uint8_t* codes, c
   }
 }
 
+// The scales once more by feature tile of the pair kernel: chunks [groups *
+// f_tiles][sup][2][512], row r of a tile's chunk r / 128 with the four bytes of
+// its feature's row block (features beyond the tile: the last block's).
+__global__ void __launch_bounds__(256) fp8_pack_pair_scales_kernel(const uint8_t* scales, int row_tiles, int rpg, int f_tiles,
+                                                                   int tile_f, int k_blocks, int sup, uint8_t* out) {
+  const int ft = blockIdx.x, r = threadIdx.x;
+  const int f = min((ft / f_tiles) * rpg + (ft % f_tiles) * tile_f + r, row_tiles * kRowTile - 1);
+  const uint8_t* s = scales + (int64_t)(f / kRowTile) * k_blocks;
+  for (int c = blockIdx.y; c < sup; c += gridDim.y) {
+    uint32_t w = 0;
+    for (int j = 0; j < 4; ++j) w |= (uint32_t)(4 * c + j < k_blocks ? s[4 * c + j] : 127) << (8 * j);
+    *reinterpret_cast<uint32_t*>(out + (((int64_t)ft * sup + c) * 2 + (r >> 7)) * kSfBytes + scale_off(r & 127)) = w;
+  }
+}
+
 __global__ void fp8_pack_end_kernel() {}
 
 // BF16 weight [n_out][kg] -> E4M3 codes and one E8M0 scale per 128 x 128
@@ -637,7 +625,7 @@ namespace {
 
 struct Plan {
   int row_tiles, k_blocks, sup, splits, nt, tok_tiles, tile_n, chunks, tiles;
-  bool fuse, spread;
+  bool fuse, spread, pair;
   size_t xp, xsf, total;      // workspace offsets and size
 };
 
@@ -663,20 +651,33 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
     p.nt = p.tile_n = 16;
     p.tok_tiles = 1;
   } else {
-    // the largest token tiles that still give every SM one, none larger than
-    // the tokens need; tiles of one call are equal, in steps of 16 tokens
-    constexpr int kTiles[] = {224, 128, 64, 32};
-    for (int i = n_tok <= 32 ? 3 : n_tok <= 64 ? 2 : n_tok <= 128 ? 1 : 0; i < (n_tok <= 32 ? 4 : 3); ++i) {
-      p.nt = kTiles[i];
+    // pairs of SMs beyond 128 tokens, unless their tiles of 256 tokens are so
+    // few that single SMs finish first (512 tokens x 2368 features: 22 pairs
+    // and 133 SMs take the same time)
+    const int m_tiles = (n_tok + 2 * kRowTile - 1) / (2 * kRowTile);
+    const int64_t pairs = (int64_t)groups * pair_tiles(n_out / groups) * m_tiles;
+    p.pair = n_tok > kRowTile && 6 * pairs > sms;
+    if (p.pair) {
+      p.nt = p.tile_n = kRowTile;
+      p.tok_tiles = 2 * m_tiles;
+    } else if (n_tok <= 64) {
+      p.nt = n_tok <= 32 ? 32 : 64;
+      p.tok_tiles = 1;
+      p.tile_n = (n_tok + 15) / 16 * 16;
+    } else {
+      // token tiles of at most 128: as many as the SMs take at once
+      p.nt = 128;
       p.tok_tiles = (n_tok + p.nt - 1) / p.nt;
-      if ((int64_t)p.row_tiles * p.tok_tiles >= sms) break;
+      const int most = std::min(sms / p.row_tiles, (n_tok + 31) / 32);
+      if (p.tok_tiles < most && n_tok > p.nt) p.tok_tiles = most;
+      p.tile_n = ((n_tok + p.tok_tiles - 1) / p.tok_tiles + 15) / 16 * 16;
+      p.tok_tiles = (n_tok + p.tile_n - 1) / p.tile_n;
     }
-    p.tile_n = ((n_tok + p.tok_tiles - 1) / p.tok_tiles + 15) / 16 * 16;
   }
   p.chunks = (p.tile_n + 127) / 128;
   p.tiles = p.row_tiles * p.tok_tiles;
   // one CTA per part where whole tiles would leave half of the SMs idle
-  p.spread = p.splits > 1 && (p.fuse || 2 * p.tiles <= sms);
+  p.spread = p.splits > 1 && !p.pair && (p.fuse || 2 * p.tiles <= sms);
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   if (!p.fuse) {
     p.xp = 0;
@@ -721,10 +722,31 @@ cudaError_t launch_nt(const Fp8Args& a, int sms, cudaStream_t st) {
 
 }  // namespace
 
-size_t fp8_weight_bytes(int n_out, int k_in, int groups) {
-  const size_t rt = (n_out + kRowTile - 1) / kRowTile, kb = (k_in / groups + kKBlk - 1) / kKBlk;
-  return rt * kb * kWTileBytes + rt * ((kb + 3) / 4) * kSfBytes;
+namespace {
+
+// A packed weight: row tiles, their scale chunks, and the scales by feature
+// tile of the pair kernel.
+struct WeightLayout {
+  int row_tiles, k_blocks, sup, f_tiles, tile_f;
+  size_t sf, pair_sf, total;
+};
+
+WeightLayout weight_layout(int n_out, int k_in, int groups) {
+  WeightLayout l{};
+  l.row_tiles = (n_out + kRowTile - 1) / kRowTile;
+  l.k_blocks = (k_in / groups + kKBlk - 1) / kKBlk;
+  l.sup = (l.k_blocks + 3) / 4;
+  l.f_tiles = pair_tiles(n_out / groups);
+  l.tile_f = pair_features(n_out / groups);
+  l.sf = (size_t)l.row_tiles * l.k_blocks * kWTileBytes;
+  l.pair_sf = l.sf + (size_t)l.row_tiles * l.sup * kSfBytes;
+  l.total = l.pair_sf + (size_t)groups * l.f_tiles * l.sup * 2 * kSfBytes;
+  return l;
 }
+
+}  // namespace
+
+size_t fp8_weight_bytes(int n_out, int k_in, int groups) { return weight_layout(n_out, k_in, groups).total; }
 
 size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok, int sms) {
   return fp8_plan(n_out, k_in, groups, n_tok, sms).total;
@@ -732,12 +754,18 @@ size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok, int sms) 
 
 cudaError_t launch_fp8_pack_weight(const uint8_t* codes, const uint8_t* scales, int n_out, int k_in, int groups,
                                    uint8_t* w, cudaStream_t st) {
-  const int kg = k_in / groups, rt = (n_out + kRowTile - 1) / kRowTile, kb = (kg + kKBlk - 1) / kKBlk;
+  const WeightLayout l = weight_layout(n_out, k_in, groups);
+  const int kg = k_in / groups;
   const bool aligned = kg % 16 == 0 && reinterpret_cast<uintptr_t>(codes) % 16 == 0;
-  fp8_pack_w_kernel<<<dim3(kb, rt), 256, 0, st>>>(codes, scales, n_out, kg, kb, (kb + 3) / 4, aligned, w,
-                                                  w + (size_t)rt * kb * kWTileBytes);
+  fp8_pack_w_kernel<<<dim3(l.k_blocks, l.row_tiles), 256, 0, st>>>(codes, scales, n_out, kg, l.k_blocks, l.sup, aligned, w,
+                                                                   w + l.sf);
   note_launch();
   cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  fp8_pack_pair_scales_kernel<<<dim3(groups * l.f_tiles, std::min(l.sup, 64)), 256, 0, st>>>(
+      scales, l.row_tiles, n_out / groups, l.f_tiles, l.tile_f, l.k_blocks, l.sup, w + l.pair_sf);
+  note_launch();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // The product reads the weight before it waits for the kernel ahead of it
   // on the stream: that kernel must not be the packing itself.
@@ -764,7 +792,8 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   const bool aligned = reinterpret_cast<uintptr_t>(x) % 16 == 0;
   Fp8Args a{};
   a.w = w;
-  a.wsf = w + (size_t)p.row_tiles * p.k_blocks * kWTileBytes;
+  const WeightLayout l = weight_layout(n_out, k_in, groups);
+  a.wsf = w + l.sf;
   a.x = x;
   a.x_aligned = aligned;
   a.kg = kg;
@@ -777,9 +806,10 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   if (p.fuse) return launch_nt<16, true>(a, sms, st);
   a.xp = base + p.xp;
   a.xsf = base + p.xsf;
-  const int64_t units = (int64_t)p.k_blocks * p.tok_tiles * p.tile_n * 8;
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)std::min<int64_t>((units + 255) / 256, 8 * sms), (unsigned)groups);
+  const int row_blocks = (p.tok_tiles * p.tile_n + 31) / 32;
+  const int per_group = std::max(1, 8 * sms / (row_blocks * groups));   // 8 blocks of threads an SM
+  lc.gridDim = dim3((unsigned)row_blocks, (unsigned)std::min(per_group, (p.k_blocks + 1) / 2), (unsigned)groups);
   lc.blockDim = dim3(256);
   lc.stream = st;
   cudaLaunchAttribute at[1];
@@ -791,11 +821,40 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
                                      p.tile_n, p.chunks, aligned, base + p.xp, base + p.xsf);
   note_launch();
   if (e != cudaSuccess) return e;
+  if (p.pair) {
+    static std::atomic<uint64_t> known{0};             // (the error word's address, per device)
+    static int32_t* err_at[64];
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    void* err = nullptr;
+    if (setup_needed(known, dev)) {
+      e = cudaGetSymbolAddress(&err, g_fp8_err);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) {
+        err_at[dev] = static_cast<int32_t*>(err);
+        setup_done(known, dev);
+      }
+    } else {
+      err = err_at[dev];
+    }
+    Fp8PairArgs b{};
+    b.w = w;
+    b.wsf = w + l.pair_sf;
+    b.xp = a.xp;
+    b.xsf = a.xsf;
+    b.n_out = n_out; b.n_tok = n_tok; b.groups = groups; b.splits = p.splits;
+    b.k_blocks = p.k_blocks; b.sup = p.sup; b.tok_tiles = p.tok_tiles;
+    b.f_tiles = l.f_tiles; b.tile_f = l.tile_f;
+    b.tiles = groups * l.f_tiles * (p.tok_tiles / 2);
+    b.out = out;
+    b.err = static_cast<int32_t*>(err);
+    return launch_fp8_pair(b, sms, st);
+  }
   switch (p.nt) {
     case 32: return launch_nt<32, false>(a, sms, st);
     case 64: return launch_nt<64, false>(a, sms, st);
-    case 128: return launch_nt<128, false>(a, sms, st);
-    default: return launch_nt<224, false>(a, sms, st);
+    default: return launch_nt<128, false>(a, sms, st);
   }
 }
 

@@ -1,0 +1,336 @@
+// The FP8 product (proj_fp8.cu) of many tokens, by pairs of SMs.
+//
+// What bounds it.  A 128 x 224 tile of one SM moves 84 KB through its shared
+// memory for every block of 128 columns (42 KB copied in, 42 KB read by the
+// MMAs), 656 cycles at 128 bytes a cycle, where the MMAs take 448.  Two SMs that
+// work on one 256 x 224 tile (tcgen05 cta_group::2) each hold 128 tokens and half
+// of the features and read 60 KB a block, 470 cycles.
+//
+// Tokens are the MMA's M here and features its N, so that a thread holds a
+// token's consecutive features and stores them 32 bytes at a time (features as
+// M left a thread one 2-byte store per token and feature: 9000 cycles a tile,
+// twice the MMAs' time at K = 1024).  An element is the same sum of the same
+// products in the same order as with the operands exchanged.
+//
+// Roles: in both CTAs warp 0 copies its own tokens and its half of the features;
+// the second CTA's warp 1 passes the completion of its copies on to the first,
+// whose warp 1 issues the scale copies and MMAs for both; warps 2-9 read the
+// accumulators (two, so that the next tile's MMAs run meanwhile).
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "proj_fp8.cuh"
+#include "tc.cuh"
+
+namespace csa {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kPairThreads = 64 + 256;
+constexpr int kHalfBytes = kPairFeatures / 2 * kKBlk;           // most bytes of a CTA's half of the features
+constexpr int kPairSf = 3 * kSfBytes;                           // scales: own tokens, all features
+constexpr int kPairStage = kWTileBytes + kHalfBytes + kPairSf;
+constexpr int kPairStages = 224 * 1024 / kPairStage;
+constexpr size_t kPairSmem = (size_t)kPairStages * kPairStage + 256 + 128;
+constexpr uint32_t kPairASf = 2 * kPairFeatures, kPairBSf = kPairASf + 4 * kSfRing;   // TMEM columns
+constexpr int kSetCols = kPairFeatures / 2;                     // accumulator columns of four warps
+static_assert(kPairBSf + 8 * kSfRing <= 512, "TMEM");
+static_assert(kPairStages >= 4 && kPairStages <= 8, "stages");
+
+// 16 consecutive features of one token, the first n of them.
+__device__ __forceinline__ void store_features(const GemmOut& out, int64_t t, int o, int n, const float* v) {
+  const OutRow y = out_row(out, o);
+  int sg = 0;
+  while (sg + 1 < out.n_seg && o >= out.seg_end[sg]) ++sg;
+  const int esz = y.bf16 ? 2 : 4;
+  char* p = static_cast<char*>(y.y) + t * y.rows * esz;
+  if (n >= 16 && o + 16 <= out.seg_end[sg] && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+    if (y.bf16) {
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      tc::st_global_32b(p, w);
+    } else {
+      tc::st_global_32b(p, reinterpret_cast<const uint32_t*>(v));
+      tc::st_global_32b(p + 32, reinterpret_cast<const uint32_t*>(v) + 8);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (e < n) out_row(out, o + e).store((int)t, v[e]);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_constant__ Fp8PairArgs a) {
+  constexpr int S = kPairStages;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + (size_t)S * kPairStage);   // first CTA: both CTAs' copies; second: its own
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_empty = acc_full + 2;                  // used in the first CTA
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* issued_slot = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  constexpr uint64_t kLimit = 1000000000ull;
+  constexpr int kBOff = kWTileBytes, kASfOff = kBOff + kHalfBytes, kBSfOff = kASfOff + kSfBytes;   // in a stage
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)(blockIdx.x & 1);              // in the cluster (two consecutive blocks)
+
+  tc::griddep_launch_dependents();
+  if (warp == 1) {
+    tc::pair_tmem_alloc(tmem_slot, 512);
+    tc::pair_tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) { tc::mbar_init(&full[s], rank == 0 ? 2 : 1); tc::mbar_init(&empty[s], 1); }
+    for (int x = 0; x < 2; ++x) { tc::mbar_init(&acc_full[x], 1); tc::mbar_init(&acc_empty[x], 16); }
+    tc::mbar_init(drain, 1);
+    *abort_flag = 0;
+    *issued_slot = 0;
+    tc::fence_mbar_init();
+  }
+  tc::tc_fence_before();
+  cluster.sync();                                      // both CTAs' barriers are set up
+  tc::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const int rpg = a.n_out / a.groups;
+  const int m_tiles = a.tok_tiles / 2;
+  const int it0 = blockIdx.x / 2, it_step = gridDim.x / 2;
+  // tile -> token pair m, group, first feature f0 (of the weight), features n (a multiple of 16)
+  auto tile = [&](int it, int& m, int& grp, int& ft, int& f0, int& n) {
+    m = it % m_tiles;
+    ft = it / m_tiles;
+    grp = ft / a.f_tiles;
+    f0 = (ft % a.f_tiles) * a.tile_f;
+    n = min(a.tile_f, (rpg - f0 + 15) / 16 * 16);
+    f0 += grp * rpg;
+  };
+  bool ok = true;
+  if (warp == 0) {
+    // ---- producer of this CTA (one thread)
+    if (tc::elect_one()) {
+      // (every instruction between two blocks counts: addresses run along)
+      uint32_t x = 0, st = 0, ph = 1;                  // (a fresh barrier's wait for phase 1 passes)
+      const int64_t xp_step = (int64_t)a.tok_tiles * kWTileBytes, xsf_step = (int64_t)a.tok_tiles * kSfBytes;
+      const uint32_t sm0 = tc::smem_u32(sm), full0 = tc::smem_u32(full);
+      tc::griddep_wait();
+      for (int it = it0; it < a.tiles && ok; it += it_step) {
+        int m, grp, ft, f0, n;
+        tile(it, m, grp, ft, f0, n);
+        const int half = n / 2, f = f0 + rank * half;
+        const int rt = f / kRowTile, r0 = f % kRowTile;
+        const uint32_t b1 = (uint32_t)min(half, kRowTile - r0) * kKBlk, b2 = (uint32_t)half * kKBlk - b1;
+        const uint8_t* w1 = a.w + (int64_t)rt * a.k_blocks * kWTileBytes + r0 * kKBlk;
+        const uint8_t* w2 = a.w + (int64_t)(rt + 1) * a.k_blocks * kWTileBytes;
+        const uint8_t* xp = a.xp + ((int64_t)grp * a.k_blocks * a.tok_tiles + 2 * m + rank) * kWTileBytes;
+        const uint8_t* xsf = a.xsf + ((int64_t)grp * a.sup * a.tok_tiles + 2 * m + rank) * kSfBytes;
+        const uint8_t* wsf = a.wsf + (int64_t)ft * a.sup * 2 * kSfBytes;
+        const uint32_t bytes = (uint32_t)kWTileBytes + b1 + b2;
+        for (int kb = 0; kb < a.k_blocks; ++kb) {
+          ok = tc::mbar_wait(&empty[st], ph, kLimit);
+          if (!ok) break;
+          const uint32_t at = sm0 + st * kPairStage, bar = full0 + st * 8;
+          if ((kb & 3) == 0) {
+            tc::mbar_expect_tx_at(bar, bytes + kPairSf);
+            tc::bulk_g2s_at(at + kASfOff, xsf, kSfBytes, bar);
+            tc::bulk_g2s_at(at + kBSfOff, wsf, 2 * kSfBytes, bar);
+            xsf += xsf_step;
+            wsf += 2 * kSfBytes;
+          } else {
+            tc::mbar_expect_tx_at(bar, bytes);
+          }
+          tc::bulk_g2s_at(at, xp, kWTileBytes, bar);
+          tc::bulk_g2s_at(at + kBOff, w1, b1, bar);
+          if (b2) tc::bulk_g2s_at(at + kBOff + b1, w2, b2, bar);
+          xp += xp_step;
+          w1 += kWTileBytes;
+          w2 += kWTileBytes;
+          ++x;
+          if (++st == S) { st = 0; ph ^= 1; }
+        }
+      }
+      *issued_slot = x;
+      if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 1) {
+    // ---- this CTA's copies of a stage have landed: tell the first CTA
+    if (tc::elect_one()) {
+      uint32_t st = 0, ph = 0;
+      for (int it = it0; it < a.tiles && ok; it += it_step)
+        for (int kb = 0; kb < a.k_blocks; ++kb) {
+          ok = tc::mbar_wait(&full[st], ph, kLimit);
+          if (!ok) break;
+          tc::mbar_arrive_cluster(&full[st], 0);
+          if (++st == S) { st = 0; ph ^= 1; }
+        }
+      if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- scale copies and MMAs of both CTAs (one thread)
+    if (tc::elect_one()) {
+      const uint32_t desc_hi = tc::smem_desc_hi(1024), sf_hi = tc::smem_desc_hi(128);
+      const uint32_t lo0 = tc::smem_desc_lo(tc::smem_u32(sm), 128);
+      constexpr uint32_t kIdStep = (1u << 29) | (1u << 4);
+      uint32_t st = 0, ph = 0, u = 0, r = kSfRing - 1;
+      for (int it = it0; it < a.tiles && ok; it += it_step) {
+        int m, grp, ft, f0, n;
+        tile(it, m, grp, ft, f0, n);
+        const uint32_t idesc0 = tc::idesc_mxf8(2 * kRowTile, n, 0, 0);
+        int kb = 0;
+        for (int q = 0; q < a.splits && ok; ++q, ++u) {
+          const int b1 = part_begin(a.k_blocks, a.splits, q + 1);
+          const uint32_t acc = tmem + (u & 1) * kPairFeatures;
+          if (u >= 2) ok = tc::mbar_wait_cluster(&acc_empty[u & 1], ((u >> 1) - 1) & 1, kLimit);
+          for (uint32_t more = 0; kb < b1; ++kb, more = 1) {
+            ok = ok && tc::mbar_wait_cluster(&full[st], ph, kLimit);
+            if (!ok) break;
+            tc::tc_fence_after();
+            // (a scale buffer is rewritten 16 blocks or two tiles after its
+            // load, when the MMAs that read it are complete)
+            const bool sf = (kb & 3) == 0;
+            if (sf) r = (r + 1) & (kSfRing - 1);
+            const uint32_t id = kb & 3, lo = lo0 + st * (kPairStage / 16);
+            const uint32_t asf = tmem + kPairASf + r * 4, bsf = tmem + kPairBSf + r * 8;
+            const uint32_t asf_id = asf | (id << 30), bsf_id = bsf | (id << 30);
+            const uint32_t idesc = idesc0 + id * kIdStep;
+            if (sf) {
+              tc::pair_tmem_cp(asf, tc::desc64(lo + kASfOff / 16, sf_hi));
+              tc::pair_tmem_cp(bsf, tc::desc64(lo + kBSfOff / 16, sf_hi));
+              tc::pair_tmem_cp(bsf + 4, tc::desc64(lo + (kBSfOff + kSfBytes) / 16, sf_hi));
+            }
+            tc::pair_mma_mxf8(acc, tc::desc64(lo, desc_hi), tc::desc64(lo + kBOff / 16, desc_hi), idesc, asf_id, bsf_id, more);
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+              tc::pair_mma_mxf8(acc, tc::desc64(lo + k * 16, desc_hi), tc::desc64(lo + kBOff / 16 + k * 16, desc_hi), idesc,
+                                asf_id, bsf_id, 1u);
+            tc::pair_commit(&empty[st]);
+            if (kb + 1 == b1) tc::pair_commit(&acc_full[u & 1]);
+            if (++st == S) { st = 0; ph ^= 1; }
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
+  } else {
+    // ---- epilogue: a thread is a token of this CTA, set 0 or 1 the features' halves
+    tc::griddep_wait();
+    const int q4 = warp & 3, set = (warp - 2) >> 2;
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    uint32_t u = 0;
+    for (int it = it0; it < a.tiles; it += it_step) {
+      int m, grp, ft, f0, n;
+      tile(it, m, grp, ft, f0, n);
+      const int64_t t = (int64_t)(2 * m + rank) * kRowTile + q4 * 32 + lane;
+      // this set's columns: the first or second half in steps of 16
+      const int c_lo = set == 0 ? 0 : (n / 16 + 1) / 2 * 16, c_n = (set == 0 ? (n / 16 + 1) / 2 * 16 : n) - c_lo;
+      const int f_end = grp * rpg + min(rpg, f0 - grp * rpg + n);
+      auto emit = [&](int c, const float* v) {
+        if (t < a.n_tok) store_features(a.out, t, f0 + c_lo + c, f_end - (f0 + c_lo + c), v);
+      };
+      if (a.splits == 1) {
+        ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        tc::tc_fence_after();
+        for (int c = 0; c < c_n; c += 16) {
+          uint32_t v[16];
+          tc::tmem_ld_x16(tmem + lane_base + (u & 1) * kPairFeatures + c_lo + c, v);
+          tc::tmem_wait_ld();
+          emit(c, reinterpret_cast<const float*>(v));
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(&acc_empty[u & 1], 0);
+        ++u;
+      } else {
+        float acc[kSetCols];
+        for (int q = 0; q < a.splits; ++q, ++u) {
+          ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
+          tc::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kSetCols; c += 16)
+            if (c < c_n) {
+              uint32_t v[16];
+              tc::tmem_ld_x16(tmem + lane_base + (u & 1) * kPairFeatures + c_lo + c, v);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[c + e] = q == 0 ? __uint_as_float(v[e]) : acc[c + e] + __uint_as_float(v[e]);
+            }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_cluster(&acc_empty[u & 1], 0);
+        }
+        if (!ok) continue;
+#pragma unroll
+        for (int c = 0; c < kSetCols; c += 16)
+          if (c < c_n) emit(c, acc + c);
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  __syncwarp();
+  if (warp == 1 && rank == 0) {
+    // no MMA of the pair is in flight when either CTA's memory is released
+    if (tc::elect_one()) tc::pair_commit_own(drain);
+    __syncwarp();
+    tc::mbar_wait(drain, 0, 200000000ull);
+  }
+  if (*abort_flag && tid == 0) {
+    if (atomicCAS(a.err, 0, (int32_t)kErrTimeout) == 0) a.err[1] = (int32_t)blockIdx.x;
+    // let the copies already issued land before the shared memory goes away
+    const uint32_t issued = *issued_slot;
+    for (uint32_t x = issued > (uint32_t)S ? issued - S : 0; x < issued; ++x)
+      tc::mbar_wait(&full[x % S], (x / S) & 1, 200000000ull);
+  }
+  tc::tc_fence_before();
+  cluster.sync();
+  if (warp == 1) tc::pair_tmem_dealloc(tmem, 512);
+  cluster.sync();
+}
+
+cudaError_t launch_fp8_pair(const Fp8PairArgs& a, int sms, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (setup_needed(attr_set, dev)) {
+    e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    if (e != cudaSuccess) return e;
+    setup_done(attr_set, dev);
+  }
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3((unsigned)(2 * std::min(a.tiles, sms / 2)));
+  lc.blockDim = dim3(kPairThreads);
+  lc.dynamicSmemBytes = kPairSmem;
+  lc.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 2;
+  e = cudaLaunchKernelEx(&lc, fp8_pair_kernel, a);
+  note_launch();
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace csa

@@ -162,12 +162,12 @@ def test_gemm_shapes_and_argument_errors_on_the_host(cuda_lib):
 
 def test_fp8_gemm_shapes_and_argument_errors_on_the_host(cuda_lib):
     """The FP8 product's size function and argument checks run on the host:
-    packed bytes are 16 KB tiles of 128 x 128 codes and 512 bytes of scales
-    per row tile and four blocks; every bad argument comes back before any
+    packed bytes are 16 KB tiles of 128 x 128 codes, 512 bytes of scales per
+    row tile and four blocks, and 1024 per feature tile (at most 224) and four; every bad argument comes back before any
     launch (the pointers below are never touched)."""
     wb = cuda_lib.csa_gemm_fp8_weight_bytes
-    assert wb(300, 1000, 1) == 3 * (8 * 16384 + 2 * 512)
-    assert wb(16 * 128, 16 * 64, 16) == 16 * (16384 + 512)
+    assert wb(300, 1000, 1) == 3 * (8 * 16384 + 2 * 512) + 2 * 2 * 1024
+    assert wb(16 * 128, 16 * 64, 16) == 16 * (16384 + 512) + 16 * 1024
     for bad in ((0, 64, 1), (256, 0, 1), (256, 64, 0), (256, 63, 1), (300, 64, 2), (256, 96, 3), (65536 * 128, 64, 1)):
         assert wb(*bad) == 0, bad
     P = 0x10000

@@ -71,6 +71,8 @@ SHAPES = [
     (38000, 8, 1, 3),             # one K block: tiles follow each other at every block
     (2048, 4096, 16, 7),          # grouped
     (512, 4 * 72, 4, 130),        # grouped, the last block of each group short
+    (6400, 10 * 264, 10, 520),    # pairs of SMs: grouped, tiles that begin inside a row tile
+    (9100, 1160, 1, 513),         # pairs of SMs: two K parts, one token beyond two tiles, a ragged last tile
 ]
 
 
