@@ -65,7 +65,8 @@ struct Fp8Args {
   int kg;
   int n_out, n_tok;
   int row_tiles, k_blocks, sup;   // sup: scale chunks along K, ceil(k_blocks / 4)
-  int groups, splits;
+  int groups, group_tiles;        // row tiles of a group
+  int splits, split_lg;           // K parts, a power of two
   int tok_tiles, tile_n;          // token tiles of tile_n tokens (a multiple of 16)
   int spread;
   int tiles;                      // row_tiles * tok_tiles
@@ -73,26 +74,34 @@ struct Fp8Args {
 };
 
 // NT: most tokens of a tile.  FUSE: the tokens are quantised by this kernel.
-template <int NT, bool FUSE>
+// ONE: one accumulator, for CTAs that work on one part of one tile (spread);
+// two CTAs of 128 tokens then share an SM's TMEM.
+template <int NT, bool FUSE, bool ONE>
 struct Cfg {
   static constexpr int kSets = NT >= 128 ? 2 : 1;          // sets of 4 epilogue warps, each a share of the columns
   static constexpr int kCols = NT / kSets;                 // accumulator columns of a set
   static constexpr int kEpi = 128 * kSets;
   static constexpr int kThreads = 64 + kEpi + (FUSE ? 128 : 0);
-  static constexpr int kPerSm = NT <= 64 ? 2 : 1;          // CTAs per SM
+  static constexpr int kAccs = ONE ? 1 : 2;
+  static constexpr int kPerSm = NT <= 64 || ONE ? 2 : 1;   // CTAs per SM
   static constexpr int kChunks = (NT + 127) / 128;         // scale chunks of a token tile
-  static constexpr int kStageBytes = kWTileBytes + NT * kKBlk + kSfBytes * (1 + kChunks);
-  static constexpr int kStagesFit = (kPerSm == 2 ? 110 : 224) * 1024 / kStageBytes;
+  // Fused: the tokens' blocks have slots of their own beside the ring, filled
+  // a batch at a time (the loads of a batch, 32 registers a thread, are in
+  // flight at once), so that the quantiser works ahead of the weight.
+  static constexpr int kBatch = 4, kBatches = 2;
+  static constexpr int kSlotBytes = NT * kKBlk + kSfBytes;
+  static constexpr int kSlots = FUSE ? kBatch * kBatches * kSlotBytes : 0;
+  static constexpr int kStageBytes = kWTileBytes + kSfBytes + (FUSE ? 0 : NT * kKBlk + kSfBytes * kChunks);
+  static constexpr int kStagesFit = ((kPerSm == 2 ? 110 : 224) * 1024 - kSlots) / kStageBytes;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
-  static constexpr int kBatch = 4;                         // fused: blocks a thread loads at once (32 registers)
-  // TMEM: two accumulators, the weight's scale ring, the tokens' scale ring
+  // TMEM: the accumulators, the weight's scale ring, the tokens' scale ring
   static constexpr uint32_t kXsfRing = FUSE ? 8 : kSfRing;
-  static constexpr uint32_t kWsfBase = 2 * NT, kXsfBase = kWsfBase + 4 * kSfRing;
+  static constexpr uint32_t kWsfBase = kAccs * NT, kXsfBase = kWsfBase + 4 * kSfRing;
   static constexpr uint32_t kColsNeeded = kXsfBase + 4 * kChunks * kXsfRing;
   static constexpr uint32_t kTmemCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 256 + 128;   // ring, barriers, alignment
+  static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kSlots + 256 + 128;   // ring, barriers, alignment
   static_assert(kColsNeeded <= 512 && kTmemCols * kPerSm <= 512, "TMEM");
-  static_assert(kStages >= 3 && kStages <= 8 && kBatch <= kStages, "stages");
+  static_assert(kStages >= 3 && kStages <= 8, "stages");
   static_assert(!FUSE || NT == 16, "a quantising thread takes one unit of a block");
   static_assert(kRowTile * NT * 4 <= kStages * kStageBytes, "a part's sums fit in the ring");
 };
@@ -204,26 +213,30 @@ __global__ void __launch_bounds__(256) fp8_quant_x_kernel(const uint16_t* x, int
 
 // Warp 0 issues the bulk copies, warp 1 the scale copies and MMAs, the next 4 or 8 read the accumulators (a thread = one output
 // feature, its columns = tokens), the last 4 (FUSE) quantise the tokens.
-template <int NT, bool FUSE>
-__global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm)
+template <int NT, bool FUSE, bool ONE>
+__global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ONE>::kPerSm)
     fp8_gemm_kernel(const __grid_constant__ Fp8Args a) {
-  using C = Cfg<NT, FUSE>;
+  using C = Cfg<NT, FUSE, ONE>;
+  constexpr uint32_t kAccMask = C::kAccs - 1;
   constexpr int S = C::kStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + (size_t)S * C::kStageBytes);
+  uint8_t* slots = sm + (size_t)S * C::kStageBytes;    // fused: the tokens' blocks
+  uint64_t* full = reinterpret_cast<uint64_t*>(slots + C::kSlots);
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* x_full = drain + 1;                        // fused: a batch of slots is filled, is read
+  uint64_t* x_empty = x_full + C::kBatches;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_empty + C::kBatches);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* issued_slot = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);   // stages the producer filled
   // (broadcast: the role and the TMEM base are then known to be warp-uniform,
   // and the MMAs' operands need no move between register files)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr uint64_t kLimit = 1000000000ull;
-  constexpr int kXOff = kWTileBytes, kWsfOff = kXOff + NT * kKBlk, kXsfOff = kWsfOff + kSfBytes;   // in a stage
+  constexpr int kXOff = kWTileBytes, kWsfOff = kXOff + (FUSE ? 0 : NT * kKBlk), kXsfOff = kWsfOff + kSfBytes;   // in a stage
 
   tc::griddep_launch_dependents();
   if (warp == 1) {
@@ -231,9 +244,10 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) { tc::mbar_init(&full[s], FUSE ? 5 : 1); tc::mbar_init(&empty[s], 1); }
+    for (int s = 0; s < S; ++s) { tc::mbar_init(&full[s], 1); tc::mbar_init(&empty[s], 1); }
     for (int x = 0; x < 2; ++x) { tc::mbar_init(&acc_full[x], 1); tc::mbar_init(&acc_empty[x], C::kEpi); }
     tc::mbar_init(drain, 1);
+    for (int b = 0; b < C::kBatches; ++b) { tc::mbar_init(&x_full[b], 4); tc::mbar_init(&x_empty[b], 1); }
     *abort_flag = 0;
     *issued_slot = 0;
     tc::fence_mbar_init();
@@ -242,18 +256,20 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const int rows_per_group = a.n_out / a.groups;
+  const uint32_t lg = (uint32_t)a.split_lg;
   const int xb = a.tile_n * kKBlk;                      // bytes of one packed activation block
   const int n_sfb = (a.tile_n + 127) / 128;             // its scale chunks
 
   // Spread: this CTA's part of one tile.  Whole: every part of the tiles
   // blockIdx.x, blockIdx.x + gridDim.x, ...
-  const int part = a.spread ? (int)(blockIdx.x % a.splits) : 0;
-  const int it0 = a.spread ? (int)(blockIdx.x / a.splits) : (int)blockIdx.x;
+  const int part = a.spread ? (int)(blockIdx.x & (a.splits - 1)) : 0;
+  const int it0 = a.spread ? (int)(blockIdx.x >> lg) : (int)blockIdx.x;
   const int it_step = a.spread ? a.tiles : (int)gridDim.x;
-  const int k0 = a.spread ? part_begin(a.k_blocks, a.splits, part) : 0;
-  const int k1 = a.spread ? part_begin(a.k_blocks, a.splits, part + 1) : a.k_blocks;
+  const int k0 = a.spread ? part_begin(a.k_blocks, lg, part) : 0;
+  const int k1 = a.spread ? part_begin(a.k_blocks, lg, part + 1) : a.k_blocks;
   const int q0 = part, q1 = a.spread ? part + 1 : a.splits;
+  auto row_tile = [&](int it) { return FUSE || a.tok_tiles == 1 ? it : it / a.tok_tiles; };
+  auto group = [&](int rt) { return a.groups == 1 ? 0 : rt / a.group_tiles; };
   bool ok = true;
   if (warp == 0) {
     // ---- producer (one thread).  The weight does not depend on the kernels
@@ -268,7 +284,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
       uint32_t x = 0, st = 0, ph = 1;                   // stages filled; the stage and its last release's phase
       const int pre = k1 - k0 < S ? k1 - k0 : S;        // blocks whose weight copies are issued ahead
       {
-        const int rt = it0 / a.tok_tiles;
+        const int rt = row_tile(it0);
         const uint8_t* w = a.w + ((int64_t)rt * a.k_blocks + k0) * kWTileBytes;
         const uint8_t* wsf = a.wsf + ((int64_t)rt * a.sup + (k0 >> 2)) * kSfBytes;
         for (int i = 0; i < pre; ++i, w += kWTileBytes) {
@@ -284,8 +300,8 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
       }
       if (!FUSE) tc::griddep_wait();
       for (int it = it0; it < a.tiles && ok; it += it_step) {
-        const int rt = it / a.tok_tiles, tt = it % a.tok_tiles;
-        const int64_t grp = (rt * kRowTile) / rows_per_group;
+        const int rt = row_tile(it), tt = it - rt * a.tok_tiles;
+        const int64_t grp = group(rt);
         const uint8_t* w = a.w + ((int64_t)rt * a.k_blocks + k0) * kWTileBytes;
         const uint8_t* wsf = a.wsf + ((int64_t)rt * a.sup + (k0 >> 2)) * kSfBytes;
         const uint8_t* xp = a.xp + ((grp * a.k_blocks + k0) * a.tok_tiles + tt) * xb;
@@ -334,14 +350,17 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
       uint32_t st = 0, ph = 0;                          // stage and its phase
       uint32_t u = 0;                                   // accumulators used
       uint32_t wr = kSfRing - 1, xr = FUSE ? 0 : kSfRing - 1;   // scale buffers in use
+      uint32_t xbatch = 0, xi = 0, xph = 0;             // fused: the tokens' batch, the block in it, its phase
+      const uint32_t slot0 = tc::smem_desc_lo(tc::smem_u32(slots), 128);
       for (int it = it0; it < a.tiles && ok; it += it_step) {
         int kb = k0;
         for (int q = q0; q < q1 && ok; ++q, ++u) {
-          const int b1 = part_begin(a.k_blocks, a.splits, q + 1);
-          const uint32_t acc = tmem + (u & 1) * NT;
-          if (u >= 2) ok = tc::mbar_wait(&acc_empty[u & 1], ((u >> 1) - 1) & 1, kLimit);
+          const int b1 = part_begin(a.k_blocks, lg, q + 1);
+          const uint32_t acc = tmem + (u & kAccMask) * NT;
+          if (!ONE && u >= 2) ok = tc::mbar_wait(&acc_empty[u & 1], ((u >> 1) - 1) & 1, kLimit);
           for (uint32_t more = 0; kb < b1; ++kb, more = 1) {
             ok = ok && tc::mbar_wait(&full[st], ph, kLimit);
+            if (FUSE && xi == 0) ok = ok && tc::mbar_wait(&x_full[xbatch], xph, kLimit);
             if (!ok) break;
             tc::tc_fence_after();
             // A scale buffer of four blocks is rewritten four loads after its
@@ -355,6 +374,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
               if (!FUSE) xr = wr;
             }
             const uint32_t id = kb & 3, lo = lo0 + st * (C::kStageBytes / 16);
+            const uint32_t xlo = FUSE ? slot0 + (xbatch * C::kBatch + xi) * (C::kSlotBytes / 16) : lo + kXOff / 16;
             const uint32_t wsf = tmem + C::kWsfBase + wr * 4, xsf = tmem + C::kXsfBase + xr * 4 * C::kChunks;
             const uint32_t wsf_id = wsf | (id << 30), xsf_id = FUSE ? xsf : xsf | (id << 30);
             const uint32_t idesc = idesc0 + id * kIdStep;
@@ -362,16 +382,27 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
             if (FUSE || sf) {
 #pragma unroll
               for (int ch = 0; ch < C::kChunks; ++ch)
-                if (ch < n_sfb) tc::tmem_cp_32x128b_x4(xsf + 4 * ch, tc::desc64(lo + (kXsfOff + kSfBytes * ch) / 16, sf_hi));
+                if (ch < n_sfb)
+                  tc::tmem_cp_32x128b_x4(xsf + 4 * ch, tc::desc64(FUSE ? xlo + NT * kKBlk / 16 : lo + (kXsfOff + kSfBytes * ch) / 16, sf_hi));
             }
-            tc::mma_mxf8(acc, tc::desc64(lo, desc_hi), tc::desc64(lo + kXOff / 16, desc_hi), idesc, wsf_id, xsf_id, more);
+            tc::mma_mxf8(acc, tc::desc64(lo, desc_hi), tc::desc64(xlo, desc_hi), idesc, wsf_id, xsf_id, more);
 #pragma unroll
             for (int m = 1; m < 4; ++m)
-              tc::mma_mxf8(acc, tc::desc64(lo + m * 16, desc_hi), tc::desc64(lo + kXOff / 16 + m * 16, desc_hi), idesc, wsf_id,
+              tc::mma_mxf8(acc, tc::desc64(lo + m * 16, desc_hi), tc::desc64(xlo + m * 16, desc_hi), idesc, wsf_id,
                            xsf_id, 1u);
             tc::mma_commit(&empty[st]);
-            if (kb + 1 == b1) tc::mma_commit(&acc_full[u & 1]);
-            if (FUSE) xr = (xr + 1) & (C::kXsfRing - 1);
+            if (kb + 1 == b1) tc::mma_commit(&acc_full[u & kAccMask]);
+            if (FUSE) {
+              xr = (xr + 1) & (C::kXsfRing - 1);
+              // (the batch is counted, not derived from a slot number: with
+              // x_empty[slot / 4] under slot % 4 == 3 this commit faulted on
+              // a misaligned barrier address)
+              if (++xi == C::kBatch) {
+                tc::mma_commit(&x_empty[xbatch]);
+                xi = 0;
+                if (++xbatch == C::kBatches) { xbatch = 0; xph ^= 1; }
+              }
+            }
             if (++st == S) { st = 0; ph ^= 1; }
           }
         }
@@ -393,37 +424,31 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
     int lit = it0, lkb = k0;                            // the next block to load
     Unit v[C::kBatch];
     auto load = [&](Unit& dst) {
-      const int64_t grp = (lit * kRowTile) / rows_per_group;
+      const int64_t grp = group(lit);
       const int col = lkb * kKBlk + c * 16;
       const bool there = lit < a.tiles && r < a.n_tok;
       dst = load_unit(a.x + (there ? r : 0) * row_len + grp * a.kg + col, there ? a.kg - col : 0, a.x_aligned != 0);
       if (++lkb == k1) { lkb = k0; lit += it_step; }
     };
+    uint32_t batch = 0, ph = 1;                          // (a fresh barrier's wait for phase 1 passes)
     for (int j0 = 0; j0 < total && ok; j0 += C::kBatch) {
 #pragma unroll
       for (int d = 0; d < C::kBatch; ++d) load(v[d]);   // (past the last block: zeros, not used)
+      ok = tc::mbar_wait(&x_empty[batch], ph, kLimit) && !*abort_flag;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      uint8_t* at = slots + batch * C::kBatch * C::kSlotBytes;
 #pragma unroll
-      for (int d = 0; d < C::kBatch; ++d) {
-        const uint32_t x = (uint32_t)(j0 + d);
-        if (j0 + d < total && ok) {
-          if (x >= (uint32_t)S) ok = tc::mbar_wait(&empty[x % S], ((x / S) - 1) & 1, kLimit) && !*abort_flag;
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            uint8_t* st = sm + (size_t)(x % S) * C::kStageBytes;
-            uint4 codes;
-            const uint32_t sf = quant_unit(v[d], codes);
-            *reinterpret_cast<uint4*>(st + kXOff + code_off(r, c)) = codes;
-            if (c == 0) *reinterpret_cast<uint32_t*>(st + kXsfOff + scale_off(r)) = sf;
-          }
-        }
+      for (int d = 0; d < C::kBatch; ++d, at += C::kSlotBytes) {
+        uint4 codes;
+        const uint32_t sf = quant_unit(v[d], codes);
+        *reinterpret_cast<uint4*>(at + code_off(r, c)) = codes;
+        if (c == 0) *reinterpret_cast<uint32_t*>(at + NT * kKBlk + scale_off(r)) = sf;
       }
-      if (ok) {
-        tc::fence_proxy_async_smem();                   // (the MMA reads them through the async proxy)
-        __syncwarp();
-#pragma unroll
-        for (int d = 0; d < C::kBatch; ++d)
-          if (lane == 0 && j0 + d < total) tc::mbar_arrive(&full[(uint32_t)(j0 + d) % S]);
-      }
+      tc::fence_proxy_async_smem();                     // (the MMA reads them through the async proxy)
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&x_full[batch]);
+      if (++batch == C::kBatches) { batch = 0; ph ^= 1; }
     }
     if (!ok) *abort_flag = 1;
   } else {
@@ -434,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
     const int c_lo = set * C::kCols;
     uint32_t u = 0;
     for (int it = it0; it < a.tiles; it += it_step) {
-      const int rt = it / a.tok_tiles, tt = it % a.tok_tiles;
+      const int rt = row_tile(it), tt = it - rt * a.tok_tiles;
       const int o = rt * kRowTile + q4 * 32 + lane;
       const int t0 = tt * a.tile_n;
       const int n_here = min(a.tile_n, a.n_tok - t0) - c_lo;      // this set's tokens (may be <= 0)
@@ -452,19 +477,19 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
           y.store16(t0 + c_lo + c0, n_here - c0, v);
         }
       };
-      if (FUSE || q1 - q0 == 1) {
-        ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit) && !*abort_flag;
+      if (FUSE || ONE || q1 - q0 == 1) {
+        ok = ok && tc::mbar_wait(&acc_full[u & kAccMask], ONE ? 0 : (u >> 1) & 1, kLimit) && !*abort_flag;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         tc::tc_fence_after();
         for (int c0 = 0; c0 < C::kCols && c0 < n_here; c0 += 16) {
           uint32_t v[16];
-          tc::tmem_ld_x16(tmem + lane_base + (u & 1) * NT + c_lo + c0, v);
+          tc::tmem_ld_x16(tmem + lane_base + (u & kAccMask) * NT + c_lo + c0, v);
           tc::tmem_wait_ld();
           emit(c0, reinterpret_cast<const float*>(v));
         }
         tc::tc_fence_before();
-        tc::mbar_arrive(&acc_empty[u & 1]);
+        if (!ONE) tc::mbar_arrive(&acc_empty[u & 1]);
         ++u;
       } else {
         float acc[C::kCols];
@@ -501,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE>::kThreads, Cfg<NT, FUSE>::kPerSm
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     const int et = tid - 64;
-    const int rt = it0 / a.tok_tiles, t0 = (it0 % a.tok_tiles) * a.tile_n;
+    const int rt = row_tile(it0), t0 = (it0 - rt * a.tok_tiles) * a.tile_n;
     const int f = et & (kRowTile - 1), o = rt * kRowTile + f;
     if (et >= 0 && et < C::kEpi && o < a.n_out && !*abort_flag) {
       const int n_here = min(a.tile_n, a.n_tok - t0);
@@ -687,17 +712,17 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
   return p;
 }
 
-template <int NT, bool FUSE>
+template <int NT, bool FUSE, bool ONE>
 cudaError_t launch_nt(const Fp8Args& a, int sms, cudaStream_t st) {
-  using C = Cfg<NT, FUSE>;
+  using C = Cfg<NT, FUSE, ONE>;
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (setup_needed(attr_set, dev)) {
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<NT, FUSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    e = cudaFuncSetAttribute(fp8_gemm_kernel<NT, FUSE, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<NT, FUSE>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    e = cudaFuncSetAttribute(fp8_gemm_kernel<NT, FUSE, ONE>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
     setup_done(attr_set, dev);
   }
@@ -714,7 +739,7 @@ cudaError_t launch_nt(const Fp8Args& a, int sms, cudaStream_t st) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   lc.attrs = at;
   lc.numAttrs = a.spread ? 2 : 1;
-  e = cudaLaunchKernelEx(&lc, fp8_gemm_kernel<NT, FUSE>, a);
+  e = cudaLaunchKernelEx(&lc, fp8_gemm_kernel<NT, FUSE, ONE>, a);
   note_launch();
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -799,11 +824,13 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   a.kg = kg;
   a.n_out = n_out; a.n_tok = n_tok;
   a.row_tiles = p.row_tiles; a.k_blocks = p.k_blocks; a.sup = p.sup;
-  a.groups = groups; a.splits = p.splits;
+  a.groups = groups; a.group_tiles = groups > 1 ? n_out / groups / kRowTile : p.row_tiles;
+  a.splits = p.splits;
+  while (1 << a.split_lg < p.splits) ++a.split_lg;
   a.tok_tiles = p.tok_tiles; a.tile_n = p.tile_n;
   a.spread = p.spread; a.tiles = p.tiles;
   a.out = out;
-  if (p.fuse) return launch_nt<16, true>(a, sms, st);
+  if (p.fuse) return launch_nt<16, true, false>(a, sms, st);
   a.xp = base + p.xp;
   a.xsf = base + p.xsf;
   cudaLaunchConfig_t lc{};
@@ -843,7 +870,7 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
     b.wsf = w + l.pair_sf;
     b.xp = a.xp;
     b.xsf = a.xsf;
-    b.n_out = n_out; b.n_tok = n_tok; b.groups = groups; b.splits = p.splits;
+    b.n_out = n_out; b.n_tok = n_tok; b.groups = groups; b.split_lg = a.split_lg;
     b.k_blocks = p.k_blocks; b.sup = p.sup; b.tok_tiles = p.tok_tiles;
     b.f_tiles = l.f_tiles; b.tile_f = l.tile_f;
     b.tiles = groups * l.f_tiles * (p.tok_tiles / 2);
@@ -852,9 +879,9 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
     return launch_fp8_pair(b, sms, st);
   }
   switch (p.nt) {
-    case 32: return launch_nt<32, false>(a, sms, st);
-    case 64: return launch_nt<64, false>(a, sms, st);
-    default: return launch_nt<128, false>(a, sms, st);
+    case 32: return launch_nt<32, false, false>(a, sms, st);
+    case 64: return launch_nt<64, false, false>(a, sms, st);
+    default: return p.spread ? launch_nt<128, false, true>(a, sms, st) : launch_nt<128, false, false>(a, sms, st);
   }
 }
 

@@ -107,12 +107,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
   const int rpg = a.n_out / a.groups;
   const int m_tiles = a.tok_tiles / 2;
   const int it0 = blockIdx.x / 2, it_step = gridDim.x / 2;
-  // tile -> token pair m, group, first feature f0 (of the weight), features n (a multiple of 16)
-  auto tile = [&](int it, int& m, int& grp, int& ft, int& f0, int& n) {
-    m = it % m_tiles;
-    ft = it / m_tiles;
-    grp = ft / a.f_tiles;
-    f0 = (ft % a.f_tiles) * a.tile_f;
+  // The tiles of this pair: token pair m and feature tile ft, stepped without
+  // divisions; group, first feature f0 (of the weight), features n (a multiple
+  // of 16).
+  struct Walk {
+    int it, m, ft, dm, dft;
+  };
+  Walk wk{it0, it0 % m_tiles, it0 / m_tiles, it_step % m_tiles, it_step / m_tiles};
+  auto next = [&]() {
+    wk.it += it_step;
+    wk.m += wk.dm;
+    wk.ft += wk.dft;
+    if (wk.m >= m_tiles) { wk.m -= m_tiles; ++wk.ft; }
+  };
+  auto tile = [&](int& grp, int& f0, int& n) {
+    grp = a.groups == 1 ? 0 : wk.ft / a.f_tiles;
+    f0 = (wk.ft - grp * a.f_tiles) * a.tile_f;
     n = min(a.tile_f, (rpg - f0 + 15) / 16 * 16);
     f0 += grp * rpg;
   };
@@ -125,9 +135,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const int64_t xp_step = (int64_t)a.tok_tiles * kWTileBytes, xsf_step = (int64_t)a.tok_tiles * kSfBytes;
       const uint32_t sm0 = tc::smem_u32(sm), full0 = tc::smem_u32(full);
       tc::griddep_wait();
-      for (int it = it0; it < a.tiles && ok; it += it_step) {
-        int m, grp, ft, f0, n;
-        tile(it, m, grp, ft, f0, n);
+      for (; wk.it < a.tiles && ok; next()) {
+        int grp, f0, n;
+        tile(grp, f0, n);
+        const int m = wk.m;
         const int half = n / 2, f = f0 + rank * half;
         const int rt = f / kRowTile, r0 = f % kRowTile;
         const uint32_t b1 = (uint32_t)min(half, kRowTile - r0) * kKBlk, b2 = (uint32_t)half * kKBlk - b1;
@@ -135,7 +146,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         const uint8_t* w2 = a.w + (int64_t)(rt + 1) * a.k_blocks * kWTileBytes;
         const uint8_t* xp = a.xp + ((int64_t)grp * a.k_blocks * a.tok_tiles + 2 * m + rank) * kWTileBytes;
         const uint8_t* xsf = a.xsf + ((int64_t)grp * a.sup * a.tok_tiles + 2 * m + rank) * kSfBytes;
-        const uint8_t* wsf = a.wsf + (int64_t)ft * a.sup * 2 * kSfBytes;
+        const uint8_t* wsf = a.wsf + (int64_t)wk.ft * a.sup * 2 * kSfBytes;
         const uint32_t bytes = (uint32_t)kWTileBytes + b1 + b2;
         for (int kb = 0; kb < a.k_blocks; ++kb) {
           ok = tc::mbar_wait(&empty[st], ph, kLimit);
@@ -185,13 +196,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       const uint32_t lo0 = tc::smem_desc_lo(tc::smem_u32(sm), 128);
       constexpr uint32_t kIdStep = (1u << 29) | (1u << 4);
       uint32_t st = 0, ph = 0, u = 0, r = kSfRing - 1;
-      for (int it = it0; it < a.tiles && ok; it += it_step) {
-        int m, grp, ft, f0, n;
-        tile(it, m, grp, ft, f0, n);
+      for (; wk.it < a.tiles && ok; next()) {
+        int grp, f0, n;
+        tile(grp, f0, n);
         const uint32_t idesc0 = tc::idesc_mxf8(2 * kRowTile, n, 0, 0);
         int kb = 0;
-        for (int q = 0; q < a.splits && ok; ++q, ++u) {
-          const int b1 = part_begin(a.k_blocks, a.splits, q + 1);
+        for (int q = 0; q < 1 << a.split_lg && ok; ++q, ++u) {
+          const int b1 = part_begin(a.k_blocks, a.split_lg, q + 1);
           const uint32_t acc = tmem + (u & 1) * kPairFeatures;
           if (u >= 2) ok = tc::mbar_wait_cluster(&acc_empty[u & 1], ((u >> 1) - 1) & 1, kLimit);
           for (uint32_t more = 0; kb < b1; ++kb, more = 1) {
@@ -231,17 +242,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     const int q4 = warp & 3, set = (warp - 2) >> 2;
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     uint32_t u = 0;
-    for (int it = it0; it < a.tiles; it += it_step) {
-      int m, grp, ft, f0, n;
-      tile(it, m, grp, ft, f0, n);
-      const int64_t t = (int64_t)(2 * m + rank) * kRowTile + q4 * 32 + lane;
+    for (; wk.it < a.tiles; next()) {
+      int grp, f0, n;
+      tile(grp, f0, n);
+      const int64_t t = (int64_t)(2 * wk.m + rank) * kRowTile + q4 * 32 + lane;
       // this set's columns: the first or second half in steps of 16
       const int c_lo = set == 0 ? 0 : (n / 16 + 1) / 2 * 16, c_n = (set == 0 ? (n / 16 + 1) / 2 * 16 : n) - c_lo;
       const int f_end = grp * rpg + min(rpg, f0 - grp * rpg + n);
       auto emit = [&](int c, const float* v) {
         if (t < a.n_tok) store_features(a.out, t, f0 + c_lo + c, f_end - (f0 + c_lo + c), v);
       };
-      if (a.splits == 1) {
+      if (a.split_lg == 0) {
         ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         ++u;
       } else {
         float acc[kSetCols];
-        for (int q = 0; q < a.splits; ++q, ++u) {
+        for (int q = 0; q < 1 << a.split_lg; ++q, ++u) {
           ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;
