@@ -70,6 +70,7 @@ struct Fp8Args {
   int tok_tiles, tile_n;          // token tiles of tile_n tokens (a multiple of 16)
   int spread;
   int tiles;                      // row_tiles * tok_tiles
+  int quant_groups;               // fused: groups of quantising warps, 1 or 2
   GemmOut out;
 };
 
@@ -81,13 +82,15 @@ struct Cfg {
   static constexpr int kSets = NT >= 128 ? 2 : 1;          // sets of 4 epilogue warps, each a share of the columns
   static constexpr int kCols = NT / kSets;                 // accumulator columns of a set
   static constexpr int kEpi = 128 * kSets;
-  static constexpr int kThreads = 64 + kEpi + (FUSE ? 128 : 0);
+  static constexpr int kThreads = 64 + kEpi + (FUSE ? 256 : 0);
   static constexpr int kAccs = ONE ? 1 : 2;
   static constexpr int kPerSm = NT <= 64 || ONE ? 2 : 1;   // CTAs per SM
   static constexpr int kChunks = (NT + 127) / 128;         // scale chunks of a token tile
   // Fused: the tokens' blocks have slots of their own beside the ring, filled
   // a batch at a time (the loads of a batch, 32 registers a thread, are in
-  // flight at once), so that the quantiser works ahead of the weight.
+  // flight at once) by four warps, so that the quantiser works ahead of the
+  // weight.  Long parts get a second group of four warps, whose loads are under
+  // way while the first's batch is quantised (quant_groups).
   static constexpr int kBatch = 4, kBatches = 2;
   static constexpr int kSlotBytes = NT * kKBlk + kSfBytes;
   static constexpr int kSlots = FUSE ? kBatch * kBatches * kSlotBytes : 0;
@@ -102,6 +105,7 @@ struct Cfg {
   static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kSlots + 256 + 128;   // ring, barriers, alignment
   static_assert(kColsNeeded <= 512 && kTmemCols * kPerSm <= 512, "TMEM");
   static_assert(kStages >= 3 && kStages <= 8, "stages");
+  static_assert(kBatches == 2, "one batch of slots for each group of quantising warps");
   static_assert(!FUSE || NT == 16, "a quantising thread takes one unit of a block");
   static_assert(kRowTile * NT * 4 <= kStages * kStageBytes, "a part's sums fit in the ring");
 };
@@ -212,7 +216,8 @@ __global__ void __launch_bounds__(256) fp8_quant_x_kernel(const uint16_t* x, int
 }
 
 // Warp 0 issues the bulk copies, warp 1 the scale copies and MMAs, the next 4 or 8 read the accumulators (a thread = one output
-// feature, its columns = tokens), the last 4 (FUSE) quantise the tokens.
+// feature, its columns = tokens), the last 4 or 8 (FUSE)
+// quantise the tokens.
 template <int NT, bool FUSE, bool ONE>
 __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ONE>::kPerSm)
     fp8_gemm_kernel(const __grid_constant__ Fp8Args a) {
@@ -416,7 +421,8 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
     //      waits for the loads in flight, so that loading ahead across it
     //      gains nothing)
     tc::griddep_wait();
-    const int qt = tid - 64 - C::kEpi;                  // row (qt >> 5) * 4 + (qt & 3), column (qt >> 2) & 7
+    int batch = (tid - 64 - C::kEpi) >> 7;              // the slots of this group's (next) batch
+    const int qt = (tid - 64 - C::kEpi) & 127;          // row (qt >> 5) * 4 + (qt & 3), column (qt >> 2) & 7
     const int r = (qt >> 5) * 4 + (qt & 3), c = (qt >> 2) & 7;
     const int64_t row_len = (int64_t)a.groups * a.kg;
     const int n_it = it0 < a.tiles ? (a.tiles - 1 - it0) / it_step + 1 : 0;
@@ -428,12 +434,18 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
       const int col = lkb * kKBlk + c * 16;
       const bool there = lit < a.tiles && r < a.n_tok;
       dst = load_unit(a.x + (there ? r : 0) * row_len + grp * a.kg + col, there ? a.kg - col : 0, a.x_aligned != 0);
+    };
+    auto step = [&]() {
       if (++lkb == k1) { lkb = k0; lit += it_step; }
     };
-    uint32_t batch = 0, ph = 1;                          // (a fresh barrier's wait for phase 1 passes)
-    for (int j0 = 0; j0 < total && ok; j0 += C::kBatch) {
+    const bool both = a.quant_groups == 1;              // one group fills both batches of slots in turn
+    for (int d = 0; d < batch * C::kBatch; ++d) step();
+    uint32_t ph = 1;                                     // (a fresh barrier's wait for phase 1 passes)
+    for (int j0 = batch * C::kBatch; j0 < total && ok; j0 += a.quant_groups * C::kBatch) {
 #pragma unroll
-      for (int d = 0; d < C::kBatch; ++d) load(v[d]);   // (past the last block: zeros, not used)
+      for (int d = 0; d < C::kBatch; ++d, step()) load(v[d]);   // (past the last block: zeros, not used)
+      if (!both)
+        for (int d = 0; d < C::kBatch; ++d) step();
       ok = tc::mbar_wait(&x_empty[batch], ph, kLimit) && !*abort_flag;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -448,7 +460,8 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
       tc::fence_proxy_async_smem();                     // (the MMA reads them through the async proxy)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&x_full[batch]);
-      if (++batch == C::kBatches) { batch = 0; ph ^= 1; }
+      if (both) batch ^= 1;
+      if (!both || batch == 0) ph ^= 1;
     }
     if (!ok) *abort_flag = 1;
   } else {
@@ -728,7 +741,7 @@ cudaError_t launch_nt(const Fp8Args& a, int sms, cudaStream_t st) {
   }
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3((unsigned)(a.spread ? a.tiles * a.splits : std::min(a.tiles, sms * C::kPerSm)));
-  lc.blockDim = dim3(C::kThreads);
+  lc.blockDim = dim3(FUSE ? C::kThreads - 128 * (2 - a.quant_groups) : C::kThreads);
   lc.dynamicSmemBytes = C::kSmem;
   lc.stream = st;
   cudaLaunchAttribute at[2];
@@ -830,7 +843,13 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   a.tok_tiles = p.tok_tiles; a.tile_n = p.tile_n;
   a.spread = p.spread; a.tiles = p.tiles;
   a.out = out;
-  if (p.fuse) return launch_nt<16, true, false>(a, sms, st);
+  if (p.fuse) {
+    // (7168 x 16384, 32 blocks a CTA: 20.8 us with two groups, 24.5 with one;
+    // 16 groups of 1024 x 4096, 16 blocks: 14.6 and 15.1 us;
+    // 2368 x 7168, 7 blocks: 7.0 and 6.3 us)
+    a.quant_groups = (p.spread ? p.k_blocks / p.splits : p.k_blocks) >= 16 ? 2 : 1;
+    return launch_nt<16, true, false>(a, sms, st);
+  }
   a.xp = base + p.xp;
   a.xsf = base + p.xsf;
   cudaLaunchConfig_t lc{};
