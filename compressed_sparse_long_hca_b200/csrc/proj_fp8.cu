@@ -106,7 +106,7 @@ struct Cfg {
   static_assert(kColsNeeded <= 512 && kTmemCols * kPerSm <= 512, "TMEM");
   static_assert(kStages >= 3 && kStages <= 8, "stages");
   static_assert(kBatches == 2, "one batch of slots for each group of quantising warps");
-  static_assert(!FUSE || NT == 16, "a quantising thread takes one unit of a block");
+  static_assert(!FUSE || NT == kFuseTokens, "a quantising thread takes one unit of a block");
   static_assert(kRowTile * NT * 4 <= kStages * kStageBytes, "a part's sums fit in the ring");
 };
 
@@ -535,7 +535,9 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
   }
   if (a.spread) {
     // Every CTA of the cluster adds the parts, in part order, of the tokens
-    // part, part + S, ...
+    // part, part + S, ...: a thread a feature, kAtOnce tokens in flight (a
+    // thread with four features of a token, in 16-byte loads, was slower).
+    constexpr int kAtOnce = NT <= 16 ? 1 : 4;
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     const int et = tid - 64;
@@ -548,15 +550,22 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
 #pragma unroll
       for (int p = 0; p < kMaxParts; ++p)
         src[p] = cluster.map_shared_rank(reinterpret_cast<float*>(sm), p < a.splits ? p : 0) + f;
-      for (int e = part + a.splits * (et / kRowTile); e < n_here; e += a.splits * C::kSets) {
-        float v[kMaxParts];
+      const int step = a.splits * C::kSets;
+      for (int e = part + a.splits * (et / kRowTile); e < n_here; e += step * kAtOnce) {
+        float v[kAtOnce][kMaxParts];
 #pragma unroll
-        for (int p = 0; p < kMaxParts; ++p) v[p] = p < a.splits ? src[p][e * kRowTile] : 0.f;
-        float s = v[0];
+        for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
-        for (int p = 1; p < kMaxParts; ++p)
-          if (p < a.splits) s += v[p];
-        y.store(t0 + e, s);
+          for (int p = 0; p < kMaxParts; ++p)
+            v[k][p] = p < a.splits && e + k * step < n_here ? src[p][(e + k * step) * kRowTile] : 0.f;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          float s = v[k][0];
+#pragma unroll
+          for (int p = 1; p < kMaxParts; ++p)
+            if (p < a.splits) s += v[k][p];
+          if (e + k * step < n_here) y.store(t0 + e + k * step, s);
+        }
       }
     }
     cluster.sync();                                     // a CTA's memory stays until every other has read it
@@ -686,7 +695,7 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
   p.splits = fp8_splits(p.row_tiles, p.k_blocks, sms);
   p.fuse = n_tok <= kFuseTokens;
   if (p.fuse) {
-    p.nt = p.tile_n = 16;
+    p.nt = p.tile_n = kFuseTokens;
     p.tok_tiles = 1;
   } else {
     // pairs of SMs beyond 128 tokens, unless their tiles of 256 tokens are so
@@ -848,7 +857,7 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
     // 16 groups of 1024 x 4096, 16 blocks: 14.6 and 15.1 us;
     // 2368 x 7168, 7 blocks: 7.0 and 6.3 us)
     a.quant_groups = (p.spread ? p.k_blocks / p.splits : p.k_blocks) >= 16 ? 2 : 1;
-    return launch_nt<16, true, false>(a, sms, st);
+    return launch_nt<kFuseTokens, true, false>(a, sms, st);
   }
   a.xp = base + p.xp;
   a.xsf = base + p.xsf;

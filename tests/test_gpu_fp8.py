@@ -279,3 +279,27 @@ def test_refusals():
         quantize_fp8_weight(torch.zeros(8, device="cuda"))
     with pytest.raises(RuntimeError):
         quantize_fp8_weight(torch.zeros((8, 12), device="cuda"))
+
+
+@pytest.mark.parametrize("n_out,k_in,n_tok", [(2368, 1536, 6), (2368, 1536, 50), (2368, 1536, 100), (700, 300 * 8, 300), (20001, 264, 300),
+                                              (9100, 1160, 513)])
+def test_segments_that_begin_anywhere(n_out, k_in, n_tok):
+    """Segments of odd sizes, in every form of the launch: the outputs are
+    those of one segment, and nothing beside them is written."""
+    x, _, codes, scales = _inputs(n_out, k_in, 1, n_tok, 31)
+    lin = _linear(codes, scales)
+    y = torch.empty((n_tok, n_out), device="cuda")
+    lin(x.cuda(), y)
+    rows = [1, 33, 127, 130, 2, 36, 3]
+    rows.append(n_out - sum(rows))
+    bufs, outs = [], []
+    for s, r in enumerate(rows):
+        dt = torch.bfloat16 if s % 2 else torch.float32
+        bufs.append(torch.full((n_tok * r + 18,), 5.0, dtype=dt, device="cuda"))
+        outs.append(bufs[-1][9: 9 + n_tok * r].view(n_tok, r))       # off 16 bytes
+    lin(x.cuda(), outs)
+    for b, t, part in zip(bufs, outs, y.split(rows, dim=1)):
+        assert torch.equal(t, part.to(t.dtype))
+        assert bool((b[:9] == 5).all()) and bool((b[-9:] == 5).all())
+    from compressed_sparse_long_hca_b200.api import LinearFP8
+    LinearFP8.check_device_error()
