@@ -660,7 +660,7 @@ def _raw_stream(stream, index: int) -> int | None:
 
 def _on_device(index: int, call, *args) -> int:
     """call(*args) with CUDA device `index` current."""
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         return call(*args)
     with torch.cuda.device(index):
         return call(*args)
@@ -691,7 +691,8 @@ class LinearFP8:
     [ceil(n_out / 128)][ceil(k_in / groups / 128)] of E8M0 scales
     (float8_e8m0fnu, or biased exponents as uint8: 2^(byte - 127)),
     contiguous.  With groups > 1 the weight is block diagonal, as Linear's.
-    LinearFP8.quantize makes both from a real weight.  Neither is kept."""
+    LinearFP8.quantize makes both from a real weight.  Neither is kept: the
+    constructor packs them (on `stream`) and waits until that is done."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, groups: int = 1, stream=None):
         self.lib = _lib.load()
@@ -717,13 +718,16 @@ class LinearFP8:
         check(_on_device(self._index, self.lib.csa_gemm_fp8_pack_weight, _ptr(codes), _ptr(scales), self.n_out, self.k_in,
                          self.groups, self.packed.data_ptr(), nbytes, _raw_stream(stream, self._index)),
               "csa_gemm_fp8_pack_weight")
+        # packed once and for all streams: later calls need not be ordered behind it
+        torch.cuda.current_stream(self.device).synchronize() if stream is None else stream.synchronize()
         self._need_bytes = {}
 
     @classmethod
     def quantize(cls, w, groups: int = 1, device: str | torch.device = "cuda", stream=None) -> "LinearFP8":
         """From a real weight [n_out][k_in // groups] (host array, or a
-        tensor; rounded to BF16 first): E4M3 codes with, per 128 x 128 block,
-        the least power-of-two scale that holds the block."""
+        tensor; rounded to BF16 first; or BF16 bit patterns as uint16): E4M3
+        codes with, per 128 x 128 block, the least power-of-two scale that
+        holds the block."""
         codes, scales = quantize_fp8_weight(w, device=device, stream=stream)
         return cls(codes, scales, groups=groups, stream=stream)
 
@@ -748,6 +752,8 @@ class LinearFP8:
         n = x.shape[0]
         segs, n_seg = b"", 0
         for t in (outs,) if isinstance(outs, torch.Tensor) else outs:
+            if not isinstance(t, torch.Tensor):
+                raise ValueError(f"outs[{n_seg}] must be a tensor")
             dt, shape = t.dtype, t.shape
             bf16 = dt is torch.bfloat16
             if not bf16 and dt is not torch.float32 or len(shape) != 2 or shape[0] != n or t.get_device() != index \
@@ -784,11 +790,12 @@ class LinearFP8:
 def quantize_fp8_weight(w, device: str | torch.device = "cuda", stream=None):
     """E4M3 codes (float8_e4m3fn [n_out, k]) and E8M0 scales (uint8 biased
     exponents [ceil(n_out / 128), ceil(k / 128)]) of a real weight [n_out, k]
-    (host array or tensor; rounded to BF16 first), through
-    csa_gemm_fp8_quant_weight.  A block with an infinity or a NaN gets the
+    (host array or tensor; rounded to BF16 first; or a host array of BF16 bit
+    patterns as uint16), through csa_gemm_fp8_quant_weight.  A block with an infinity or a NaN gets the
     NaN scale (255)."""
     if not isinstance(w, torch.Tensor):
-        w = torch.from_numpy(np.ascontiguousarray(np.asarray(w, dtype=np.float32)))
+        w = np.ascontiguousarray(w)
+        w = torch.from_numpy(w).view(torch.bfloat16) if w.dtype == np.uint16 else torch.from_numpy(w.astype(np.float32))
     if w.dim() != 2 or not w.is_floating_point():
         raise ValueError("w must be a real matrix [n_out, k]")
     if not w.is_cuda:
@@ -841,6 +848,7 @@ class HeadNorm:
         self.device = self.theta.device
         self._index = self.device.index
         self._theta = self.theta.data_ptr()
+        torch.cuda.current_stream(self.device).synchronize()     # the weights' copies: calls may come on any stream
         self._q_weight, self._k_weight = (0 if w is None else w.data_ptr() for w in (self.q_weight, self.k_weight))
         self.rotate_k = self.rotate_k and self.rope > 0
 

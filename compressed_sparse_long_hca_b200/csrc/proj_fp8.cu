@@ -863,8 +863,8 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   a.xsf = base + p.xsf;
   cudaLaunchConfig_t lc{};
   const int row_blocks = (p.tok_tiles * p.tile_n + 31) / 32;
-  const int per_group = std::max(1, 8 * sms / (row_blocks * groups));   // 8 blocks of threads an SM
-  lc.gridDim = dim3((unsigned)row_blocks, (unsigned)std::min(per_group, (p.k_blocks + 1) / 2), (unsigned)groups);
+  const int64_t per_group = std::max<int64_t>(1, 8LL * sms / ((int64_t)row_blocks * groups));   // 8 blocks of threads an SM
+  lc.gridDim = dim3((unsigned)row_blocks, (unsigned)std::min<int64_t>(per_group, (p.k_blocks + 1) / 2), (unsigned)groups);
   lc.blockDim = dim3(256);
   lc.stream = st;
   cudaLaunchAttribute at[1];
@@ -877,22 +877,6 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   note_launch();
   if (e != cudaSuccess) return e;
   if (p.pair) {
-    static std::atomic<uint64_t> known{0};             // (the error word's address, per device)
-    static int32_t* err_at[64];
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    void* err = nullptr;
-    if (setup_needed(known, dev)) {
-      e = cudaGetSymbolAddress(&err, g_fp8_err);
-      if (e != cudaSuccess) return e;
-      if (dev >= 0 && dev < 64) {
-        err_at[dev] = static_cast<int32_t*>(err);
-        setup_done(known, dev);
-      }
-    } else {
-      err = err_at[dev];
-    }
     Fp8PairArgs b{};
     b.w = w;
     b.wsf = w + l.pair_sf;
@@ -903,7 +887,6 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
     b.f_tiles = l.f_tiles; b.tile_f = l.tile_f;
     b.tiles = groups * l.f_tiles * (p.tok_tiles / 2);
     b.out = out;
-    b.err = static_cast<int32_t*>(err);
     return launch_fp8_pair(b, sms, st);
   }
   switch (p.nt) {
@@ -913,17 +896,19 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   }
 }
 
-// Read and clear the device error word (the caller has synchronised).
+// Read and clear the device error words (the caller has synchronised).
 cudaError_t fp8_read_error(int32_t* code, int32_t* detail) {
   int32_t w[2] = {0, 0};
   cudaError_t e = cudaMemcpyFromSymbol(w, g_fp8_err, sizeof w);
   if (e != cudaSuccess) return e;
-  *code = w[0];
-  *detail = w[1];
   if (w[0] != 0) {
     const int32_t z[2] = {0, 0};
     e = cudaMemcpyToSymbol(g_fp8_err, z, sizeof z);
+  } else {
+    e = fp8_pair_read_error(w);
   }
+  *code = w[0];
+  *detail = w[1];
   return e;
 }
 

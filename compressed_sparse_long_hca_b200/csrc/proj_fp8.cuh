@@ -78,9 +78,9 @@ struct Fp8PairArgs {
   int f_tiles, tile_f;    // feature tiles of a group, features of one
   int tiles;              // tiles of a call: groups * f_tiles * tok_tiles / 2
   GemmOut out;
-  int32_t* err;           // the product's device error word
 };
 
 cudaError_t launch_fp8_pair(const Fp8PairArgs& a, int sms, cudaStream_t st);
+cudaError_t fp8_pair_read_error(int32_t w[2]);      // reads and clears the pair kernel's error word
 
 }  // namespace csa

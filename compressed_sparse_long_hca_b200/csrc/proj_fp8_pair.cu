@@ -27,6 +27,9 @@ namespace csa {
 
 namespace cg = cooperative_groups;
 
+// Device error word of this kernel: first error wins.
+__device__ int32_t g_pair_err[2];
+
 namespace {
 
 constexpr int kPairThreads = 64 + 256;
@@ -40,32 +43,47 @@ constexpr int kSetCols = kPairFeatures / 2;                     // accumulator c
 static_assert(kPairBSf + 8 * kSfRing <= 512, "TMEM");
 static_assert(kPairStages >= 4 && kPairStages <= 8, "stages");
 
-// 16 consecutive features of one token, the first n of them.
-__device__ __forceinline__ void store_features(const GemmOut& out, int64_t t, int o, int n, const float* v) {
-  const OutRow y = out_row(out, o);
-  int sg = 0;
-  while (sg + 1 < out.n_seg && o >= out.seg_end[sg]) ++sg;
-  const int esz = y.bf16 ? 2 : 4;
-  char* p = static_cast<char*>(y.y) + t * y.rows * esz;
-  if (n >= 16 && o + 16 <= out.seg_end[sg] && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
-    if (y.bf16) {
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      tc::st_global_32b(p, w);
-    } else {
-      tc::st_global_32b(p, reinterpret_cast<const uint32_t*>(v));
-      tc::st_global_32b(p + 32, reinterpret_cast<const uint32_t*>(v) + 8);
-    }
-    return;
+// Stores of one token's features f, f + 1, ..., f + n - 1 (of the weight), 16 at
+// a time.  Where they lie in one segment, on 32 bytes, a chunk of 16 is one or
+// two stores; else it goes feature by feature.
+struct TokenOut {
+  const GemmOut* out;
+  int64_t t;
+  int f, n;
+  char* p;               // the token's feature f, or null: feature by feature
+  bool bf16;
+
+  __device__ __forceinline__ TokenOut(const GemmOut& o, int64_t tok, bool there, int f_, int n_)
+      : out(&o), t(tok), f(f_), n(there ? n_ : 0), p(nullptr), bf16(false) {
+    if (n <= 0) return;
+    int sg = 0;
+    while (sg + 1 < o.n_seg && f >= o.seg_end[sg]) ++sg;
+    const int r0 = sg > 0 ? o.seg_end[sg - 1] : 0;
+    bf16 = (o.bf16_mask >> sg) & 1u;
+    char* a = static_cast<char*>(o.y[sg]) + (t * (o.seg_end[sg] - r0) + (f - r0)) * (bf16 ? 2 : 4);
+    if (f + n <= o.seg_end[sg] && reinterpret_cast<uintptr_t>(a) % 32 == 0) p = a;
   }
+  __device__ __forceinline__ void put(int c, const uint32_t* v) const {       // features f + c .. f + c + 15
+    if (p != nullptr && c + 16 <= n) {
+      if (bf16) {
+        uint32_t w[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (e < n) out_row(out, o + e).store((int)t, v[e]);
-}
+        for (int e = 0; e < 8; ++e) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+          w[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        tc::st_global_32b(p + 2 * c, w);
+      } else {
+        tc::st_global_32b(p + 4 * c, v);
+        tc::st_global_32b(p + 4 * c + 32, v + 8);
+      }
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (c + e < n) out_row(*out, f + c + e).store((int)t, __uint_as_float(v[e]));
+  }
+};
 
 }  // namespace
 
@@ -249,23 +267,26 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
       // this set's columns: the first or second half in steps of 16
       const int c_lo = set == 0 ? 0 : (n / 16 + 1) / 2 * 16, c_n = (set == 0 ? (n / 16 + 1) / 2 * 16 : n) - c_lo;
       const int f_end = grp * rpg + min(rpg, f0 - grp * rpg + n);
-      auto emit = [&](int c, const float* v) {
-        if (t < a.n_tok) store_features(a.out, t, f0 + c_lo + c, f_end - (f0 + c_lo + c), v);
-      };
+      const TokenOut y(a.out, t, t < a.n_tok, f0 + c_lo, min(c_n, f_end - f0 - c_lo));
       if (a.split_lg == 0) {
         ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         tc::tc_fence_after();
+        // the accumulator is free once its last columns have been read
+        const uint32_t base = tmem + lane_base + (u & 1) * kPairFeatures + c_lo;
         for (int c = 0; c < c_n; c += 16) {
           uint32_t v[16];
-          tc::tmem_ld_x16(tmem + lane_base + (u & 1) * kPairFeatures + c_lo + c, v);
+          tc::tmem_ld_x16(base + c, v);
           tc::tmem_wait_ld();
-          emit(c, reinterpret_cast<const float*>(v));
+          if (c + 16 >= c_n) {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(&acc_empty[u & 1], 0);
+          }
+          y.put(c, v);
         }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(&acc_empty[u & 1], 0);
+        if (c_n <= 0 && lane == 0) tc::mbar_arrive_cluster(&acc_empty[u & 1], 0);
         ++u;
       } else {
         float acc[kSetCols];
@@ -290,7 +311,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         if (!ok) continue;
 #pragma unroll
         for (int c = 0; c < kSetCols; c += 16)
-          if (c < c_n) emit(c, acc + c);
+          if (c < c_n) y.put(c, reinterpret_cast<const uint32_t*>(acc) + c);
       }
     }
     if (!ok) *abort_flag = 1;
@@ -303,7 +324,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     tc::mbar_wait(drain, 0, 200000000ull);
   }
   if (*abort_flag && tid == 0) {
-    if (atomicCAS(a.err, 0, (int32_t)kErrTimeout) == 0) a.err[1] = (int32_t)blockIdx.x;
+    if (atomicCAS(&g_pair_err[0], 0, (int32_t)kErrTimeout) == 0) g_pair_err[1] = (int32_t)blockIdx.x;
     // let the copies already issued land before the shared memory goes away
     const uint32_t issued = *issued_slot;
     for (uint32_t x = issued > (uint32_t)S ? issued - S : 0; x < issued; ++x)
@@ -342,6 +363,13 @@ cudaError_t launch_fp8_pair(const Fp8PairArgs& a, int sms, cudaStream_t st) {
   note_launch();
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+cudaError_t fp8_pair_read_error(int32_t w[2]) {
+  cudaError_t e = cudaMemcpyFromSymbol(w, g_pair_err, 2 * sizeof(int32_t));
+  if (e != cudaSuccess || w[0] == 0) return e;
+  const int32_t z[2] = {0, 0};
+  return cudaMemcpyToSymbol(g_pair_err, z, sizeof z);
 }
 
 }  // namespace csa

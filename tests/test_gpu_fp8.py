@@ -109,6 +109,8 @@ def test_weight_quantisation_code_by_code():
     LinearFP8.quantize(w.float().numpy())(x.cuda(), y)        # from a host array
     _linear(want_c, want_s)(x.cuda(), z)
     assert torch.equal(y, z)
+    LinearFP8.quantize(w.view(torch.int16).numpy().view(np.uint16))(x.cuda(), z)      # BF16 bit patterns
+    assert torch.equal(y, z)
 
 
 @pytest.mark.parametrize("n_tok", [1, 40, 300])
@@ -164,13 +166,13 @@ def test_segments_of_both_types():
     _check(y, x, codes, scales, 1)
 
 
-@pytest.mark.parametrize("n_tok", [3, 300])
-def test_values_that_are_not_finite_reach_their_token_alone(n_tok):
-    x, _, codes, scales = _inputs(200, 400, 1, n_tok, 9)
+@pytest.mark.parametrize("n_tok,n_out", [(3, 200), (300, 200), (300, 17000)])
+def test_values_that_are_not_finite_reach_their_token_alone(n_tok, n_out):
+    x, _, codes, scales = _inputs(n_out, 400, 1, n_tok, 9)
     bad = x.clone()
     bad[1, 3], bad[2, 399] = float("inf"), float("nan")
     lin = _linear(codes, scales)
-    y, z = torch.empty((n_tok, 200), device="cuda"), torch.empty((n_tok, 200), device="cuda")
+    y, z = torch.empty((n_tok, n_out), device="cuda"), torch.empty((n_tok, n_out), device="cuda")
     lin(x.cuda(), y)
     lin(bad.cuda(), z)
     assert bool(z[1:3].isnan().all())
@@ -180,7 +182,8 @@ def test_values_that_are_not_finite_reach_their_token_alone(n_tok):
     nan = scales.copy()
     nan[1, 2] = 255
     _linear(codes, nan)(x.cuda(), z)
-    assert bool(z[:, 128:].isnan().all()) and torch.equal(z[:, :128], y[:, :128])
+    assert bool(z[:, 128:256].isnan().all())
+    assert torch.equal(z[:, :128], y[:, :128]) and torch.equal(z[:, 256:], y[:, 256:])
 
 
 def test_scales_at_both_ends():
@@ -303,3 +306,43 @@ def test_segments_that_begin_anywhere(n_out, k_in, n_tok):
         assert bool((b[:9] == 5).all()) and bool((b[-9:] == 5).all())
     from compressed_sparse_long_hca_b200.api import LinearFP8
     LinearFP8.check_device_error()
+
+
+FIRST_CALL_CAPTURED = """
+import sys, torch
+from compressed_sparse_long_hca_b200.api import HeadNorm, LinearFP8
+n_tok, n_out, k = (int(v) for v in sys.argv[1:])
+g = torch.Generator(device="cuda").manual_seed(1)
+lin = LinearFP8.quantize(torch.randn((n_out, k), generator=g, device="cuda"))
+x = torch.randn((n_tok, k), generator=g, device="cuda").to(torch.bfloat16)
+y, z = torch.zeros((n_tok, n_out), device="cuda"), torch.zeros((n_tok, n_out), device="cuda")
+hn = HeadNorm(k, 8)
+pos = torch.arange(n_tok, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    lin(x, y)
+    hn(pos, x[:, None], None)
+graph.replay()
+x.copy_(torch.randn((n_tok, k), generator=g, device="cuda"))
+xe = x.clone()
+graph.replay()
+lin(xe, z)
+hn(pos, xe[:, None], None)
+torch.cuda.synchronize()
+assert torch.equal(y, z) and torch.equal(x, xe)
+LinearFP8.check_device_error()
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("shape", [(4, 2368, 1024), (50, 300, 256), (300, 20000, 256)])
+def test_the_first_call_of_a_process_can_be_captured(shape):
+    """The launches' set-up (function attributes, module loading) works inside
+    a capture, too."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED, *map(str, shape)], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
