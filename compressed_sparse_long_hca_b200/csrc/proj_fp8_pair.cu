@@ -64,6 +64,7 @@ struct TokenOut {
     if (f + n <= o.seg_end[sg] && reinterpret_cast<uintptr_t>(a) % 32 == 0) p = a;
   }
   __device__ __forceinline__ void put(int c, const uint32_t* v) const {       // features f + c .. f + c + 15
+    if (c >= n) return;
     if (p != nullptr && c + 16 <= n) {
       if (bf16) {
         uint32_t w[8];
