@@ -362,52 +362,61 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
           const int b1 = part_begin(a.k_blocks, lg, q + 1);
           const uint32_t acc = tmem + (u & kAccMask) * NT;
           if (!ONE && u >= 2) ok = tc::mbar_wait(&acc_empty[u & 1], ((u >> 1) - 1) & 1, kLimit);
-          for (uint32_t more = 0; kb < b1; ++kb, more = 1) {
-            ok = ok && tc::mbar_wait(&full[st], ph, kLimit);
-            if (FUSE && xi == 0) ok = ok && tc::mbar_wait(&x_full[xbatch], xph, kLimit);
-            if (!ok) break;
-            tc::tc_fence_after();
-            // A scale buffer of four blocks is rewritten four loads after its
-            // own: by then the MMAs that read it are complete, for the stage
-            // just waited for was free (S <= 8 blocks back), or the
-            // accumulator two tiles back was.  The tokens' buffers of one
-            // block (FUSE) are rewritten 8 >= S blocks later.
-            const bool sf = kb == k0 || (kb & 3) == 0;
-            if (sf) {
-              wr = (wr + 1) & (kSfRing - 1);
-              if (!FUSE) xr = wr;
-            }
-            const uint32_t id = kb & 3, lo = lo0 + st * (C::kStageBytes / 16);
-            const uint32_t xlo = FUSE ? slot0 + (xbatch * C::kBatch + xi) * (C::kSlotBytes / 16) : lo + kXOff / 16;
-            const uint32_t wsf = tmem + C::kWsfBase + wr * 4, xsf = tmem + C::kXsfBase + xr * 4 * C::kChunks;
-            const uint32_t wsf_id = wsf | (id << 30), xsf_id = FUSE ? xsf : xsf | (id << 30);
-            const uint32_t idesc = idesc0 + id * kIdStep;
-            if (sf) tc::tmem_cp_32x128b_x4(wsf, tc::desc64(lo + kWsfOff / 16, sf_hi));
-            if (FUSE || sf) {
+          uint32_t more = 0;                            // 0: the part's first block
+          while (kb < b1 && ok) {
+            // the blocks of one scale chunk, the scale byte a constant of each copy of the code
+            const int first = kb & 3, last = min(b1 - (kb - first), 4);
 #pragma unroll
-              for (int ch = 0; ch < C::kChunks; ++ch)
-                if (ch < n_sfb)
-                  tc::tmem_cp_32x128b_x4(xsf + 4 * ch, tc::desc64(FUSE ? xlo + NT * kKBlk / 16 : lo + (kXsfOff + kSfBytes * ch) / 16, sf_hi));
-            }
-            tc::mma_mxf8(acc, tc::desc64(lo, desc_hi), tc::desc64(xlo, desc_hi), idesc, wsf_id, xsf_id, more);
-#pragma unroll
-            for (int m = 1; m < 4; ++m)
-              tc::mma_mxf8(acc, tc::desc64(lo + m * 16, desc_hi), tc::desc64(xlo + m * 16, desc_hi), idesc, wsf_id,
-                           xsf_id, 1u);
-            tc::mma_commit(&empty[st]);
-            if (kb + 1 == b1) tc::mma_commit(&acc_full[u & kAccMask]);
-            if (FUSE) {
-              xr = (xr + 1) & (C::kXsfRing - 1);
-              // (the batch is counted, not derived from a slot number: with
-              // x_empty[slot / 4] under slot % 4 == 3 this commit faulted on
-              // a misaligned barrier address)
-              if (++xi == C::kBatch) {
-                tc::mma_commit(&x_empty[xbatch]);
-                xi = 0;
-                if (++xbatch == C::kBatches) { xbatch = 0; xph ^= 1; }
+            for (int id = 0; id < 4; ++id) {
+              if (id < first || id >= last || !ok) continue;
+              ok = tc::mbar_wait(&full[st], ph, kLimit);
+              if (FUSE && xi == 0) ok = ok && tc::mbar_wait(&x_full[xbatch], xph, kLimit);
+              if (!ok) continue;
+              tc::tc_fence_after();
+              // A scale buffer of four blocks is rewritten four loads after its
+              // own: by then the MMAs that read it are complete, for the stage
+              // just waited for was free (S <= 8 blocks back), or the
+              // accumulator two tiles back was.  The tokens' buffers of one
+              // block (FUSE) are rewritten 8 >= S blocks later.
+              const bool sf = id == 0 || kb == k0;
+              if (sf) {
+                wr = (wr + 1) & (kSfRing - 1);
+                if (!FUSE) xr = wr;
               }
+              const uint32_t lo = lo0 + st * (C::kStageBytes / 16);
+              const uint32_t xlo = FUSE ? slot0 + (xbatch * C::kBatch + xi) * (C::kSlotBytes / 16) : lo + kXOff / 16;
+              const uint32_t wsf = tmem + C::kWsfBase + wr * 4, xsf = tmem + C::kXsfBase + xr * 4 * C::kChunks;
+              const uint32_t wsf_id = wsf + ((uint32_t)id << 30), xsf_id = FUSE ? xsf : xsf + ((uint32_t)id << 30);
+              const uint32_t idesc = idesc0 + id * kIdStep;
+              if (sf) tc::tmem_cp_32x128b_x4(wsf, tc::desc64(lo + kWsfOff / 16, sf_hi));
+              if (FUSE || sf) {
+#pragma unroll
+                for (int ch = 0; ch < C::kChunks; ++ch)
+                  if (ch < n_sfb)
+                    tc::tmem_cp_32x128b_x4(xsf + 4 * ch,
+                                           tc::desc64(FUSE ? xlo + NT * kKBlk / 16 : lo + (kXsfOff + kSfBytes * ch) / 16, sf_hi));
+              }
+              tc::mma_mxf8(acc, tc::desc64(lo, desc_hi), tc::desc64(xlo, desc_hi), idesc, wsf_id, xsf_id, more);
+#pragma unroll
+              for (int m = 1; m < 4; ++m)
+                tc::mma_mxf8(acc, tc::desc64(lo + m * 16, desc_hi), tc::desc64(xlo + m * 16, desc_hi), idesc, wsf_id, xsf_id, 1u);
+              tc::mma_commit(&empty[st]);
+              more = 1;
+              ++kb;
+              if (kb == b1) tc::mma_commit(&acc_full[u & kAccMask]);
+              if (FUSE) {
+                xr = (xr + 1) & (C::kXsfRing - 1);
+                // (the batch is counted, not derived from a slot number: with
+                // x_empty[slot / 4] under slot % 4 == 3 this commit faulted on
+                // a misaligned barrier address)
+                if (++xi == C::kBatch) {
+                  tc::mma_commit(&x_empty[xbatch]);
+                  xi = 0;
+                  if (++xbatch == C::kBatches) { xbatch = 0; xph ^= 1; }
+                }
+              }
+              if (++st == S) { st = 0; ph ^= 1; }
             }
-            if (++st == S) { st = 0; ph ^= 1; }
           }
         }
       }

@@ -346,3 +346,21 @@ def test_the_first_call_of_a_process_can_be_captured(shape):
     r = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED, *map(str, shape)], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_a_long_run_of_k_and_many_tokens():
+    """K parts of many scale chunks that begin inside one, and token counts at
+    the borders of the launch's forms: one token's bits in all of them."""
+    from compressed_sparse_long_hca_b200.api import LinearFP8
+    for n_out, k_in in ((520, 8 * 1500), (16512, 1160)):
+        x, w, codes, scales = _inputs(n_out, k_in, 1, 1100, 41)
+        lin = _linear(codes, scales)
+        xd = x.cuda()
+        base = torch.empty((1100, n_out), device="cuda")
+        lin(xd, base)
+        _check(base[:3], x[:3], codes, scales, 1)
+        for n in (1, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257, 511, 1025):
+            y = torch.empty((n, n_out), device="cuda")
+            lin(xd[1100 - n:], y)
+            assert torch.equal(y, base[1100 - n:]), (n_out, n)
+    LinearFP8.check_device_error()
