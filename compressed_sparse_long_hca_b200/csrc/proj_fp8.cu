@@ -34,7 +34,7 @@
 // arithmetic of the others, so a token's bits depend on its row and the weight.
 //
 // Up to 16 tokens (a weight stream) the call is one launch without scratch:
-// four warps of each CTA quantise the tokens' blocks from global memory
+// four or eight warps of each CTA quantise the tokens' blocks from global memory
 // straight into the MMA's operand layout.  Beyond that the quantised tokens
 // are worth keeping: a kernel packs them once, and the product's CTAs read
 // blocks of them by bulk copies (7168 x 16384, 37 tokens: 46 us with the
@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
   } else if (warp == 1) {
     // ---- scale copies and MMAs (one thread).  Issuing a block's four MMAs
     //      bounds narrow tiles: 680 cycles a block with descriptors built from
-    //      their fields in a warp-wide loop, 330 with one thread's loop over
-    //      uniform values, where base values plus multiples of the stage and
-    //      block are counted along (four MMAs themselves: 128 cycles at 64
-    //      tokens, 448 at 224).
+    //      their fields in a warp-wide loop, about 300 with one thread's loop
+    //      over uniform values, where base values plus multiples of the stage
+    //      and block are counted along (four MMAs themselves: 180 cycles or
+    //      less up to 64 tokens, 256 at 128).
     if (tc::elect_one()) {
       const uint32_t desc_hi = tc::smem_desc_hi(1024), sf_hi = tc::smem_desc_hi(128);
       const uint32_t lo0 = tc::smem_desc_lo(tc::smem_u32(sm), 128);

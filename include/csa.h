@@ -576,7 +576,10 @@ csa_status csa_gemm_check_device_error(csa_stream_t stream);
  *                           a BF16 segment 2-byte aligned); workspace
  *                           256-byte aligned, owned by the caller, not used
  *                           by other work until the call's kernels finish.
- *                           Asynchronous.
+ *                           w_packed is read before the kernel queued ahead
+ *                           of the call has finished: that kernel must not
+ *                           write it (csa_gemm_fp8_pack_weight ends with one
+ *                           that writes nothing).  Asynchronous.
  * Device errors are read with csa_gemm_check_device_error.
  * ------------------------------------------------------------------- */
 #define CSA_FP8_MAX_TOKENS 1048576
