@@ -43,30 +43,33 @@ constexpr int kSetCols = kPairFeatures / 2;                     // accumulator c
 static_assert(kPairBSf + 8 * kSfRing <= 512, "TMEM");
 static_assert(kPairStages >= 4 && kPairStages <= 8, "stages");
 
-// Stores of one token's features f, f + 1, ..., f + n - 1 (of the weight), 16 at
-// a time.  Where they lie in one segment, on 32 bytes, a chunk of 16 is one or
-// two stores; else it goes feature by feature.
+// Stores of a warp's tokens (t0 + lane, below n_tok), features f, f + 1, ...,
+// f + n - 1 (of the weight), 16 at a time.  Where they lie in one segment, and
+// every token's on 32 bytes, a lane stores its token's 16 in one or two stores.
+// Else the 16 x 16 values of each half of the warp are exchanged, so that a
+// store is 16 neighbouring features of two tokens.
 struct TokenOut {
   const GemmOut* out;
-  int64_t t;
-  int f, n;
-  char* p;               // the token's feature f, or null: feature by feature
-  bool bf16;
+  int t0, n_tok, f, n;
+  char* p;               // the lane's feature f, or null: no such token
+  bool bf16, wide;       // wide: 32-byte stores
 
-  __device__ __forceinline__ TokenOut(const GemmOut& o, int64_t tok, bool there, int f_, int n_)
-      : out(&o), t(tok), f(f_), n(there ? n_ : 0), p(nullptr), bf16(false) {
+  __device__ __forceinline__ TokenOut(const GemmOut& o, int t0_, int n_tok_, int f_, int n_)
+      : out(&o), t0(t0_), n_tok(n_tok_), f(f_), n(n_), p(nullptr), bf16(false), wide(false) {
     if (n <= 0) return;
     int sg = 0;
     while (sg + 1 < o.n_seg && f >= o.seg_end[sg]) ++sg;
     const int r0 = sg > 0 ? o.seg_end[sg - 1] : 0;
     bf16 = (o.bf16_mask >> sg) & 1u;
-    char* a = static_cast<char*>(o.y[sg]) + (t * (o.seg_end[sg] - r0) + (f - r0)) * (bf16 ? 2 : 4);
-    if (f + n <= o.seg_end[sg] && reinterpret_cast<uintptr_t>(a) % 32 == 0) p = a;
+    const int64_t t = t0 + (threadIdx.x & 31);
+    if (t < n_tok) p = static_cast<char*>(o.y[sg]) + (t * (o.seg_end[sg] - r0) + (f - r0)) * (bf16 ? 2 : 4);
+    wide = f + n <= o.seg_end[sg] && __all_sync(0xffffffffu, reinterpret_cast<uintptr_t>(p) % 32 == 0);
   }
   __device__ __forceinline__ void put(int c, const uint32_t* v) const {       // features f + c .. f + c + 15
     if (c >= n) return;
-    if (p != nullptr && c + 16 <= n) {
-      if (bf16) {
+    if (wide && c + 16 <= n) {
+      if (p == nullptr) {
+      } else if (bf16) {
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -78,11 +81,29 @@ struct TokenOut {
         tc::st_global_32b(p + 4 * c, v);
         tc::st_global_32b(p + 4 * c + 32, v + 8);
       }
+      __syncwarp();
       return;
     }
+    const int lane = threadIdx.x & 31, fe = lane & 15;
+    float w[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (c + e < n) out_row(*out, f + c + e).store((int)t, __uint_as_float(v[e]));
+    for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(v[e]);
+#pragma unroll
+    for (int s = 8; s > 0; s >>= 1) {
+      const bool up = lane & s;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (!(i & s)) {
+          const float got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + s], s);
+          w[i] = up ? got : w[i];
+          w[i + s] = up ? w[i + s] : got;
+        }
+    }
+    if (c + fe < n) {                                    // w[i]: this feature of token t0 + (lane & 16) + i
+      const int t = t0 + (lane & 16);
+      out_row(*out, f + c + fe).store16(t, n_tok - t, w);
+    }
+    __syncwarp();
   }
 };
 
@@ -264,11 +285,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     for (; wk.it < a.tiles; next()) {
       int grp, f0, n;
       tile(grp, f0, n);
-      const int64_t t = (int64_t)(2 * wk.m + rank) * kRowTile + q4 * 32 + lane;
+      const int t0 = (2 * wk.m + rank) * kRowTile + q4 * 32;
       // this set's columns: the first or second half in steps of 16
       const int c_lo = set == 0 ? 0 : (n / 16 + 1) / 2 * 16, c_n = (set == 0 ? (n / 16 + 1) / 2 * 16 : n) - c_lo;
       const int f_end = grp * rpg + min(rpg, f0 - grp * rpg + n);
-      const TokenOut y(a.out, t, t < a.n_tok, f0 + c_lo, min(c_n, f_end - f0 - c_lo));
+      const TokenOut y(a.out, t0, a.n_tok, f0 + c_lo, min(c_n, f_end - f0 - c_lo));
       if (a.split_lg == 0) {
         ok = ok && tc::mbar_wait(&acc_full[u & 1], (u >> 1) & 1, kLimit);
         ok = __all_sync(0xffffffffu, ok);
