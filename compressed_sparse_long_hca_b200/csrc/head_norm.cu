@@ -13,7 +13,8 @@
 // shadow of the loads, and every further head reuses them; the next heads'
 // loads are issued before the present ones are worked on (4 blocks of 128
 // threads an SM: the registers that the loads in flight take are worth more
-// than more blocks).  4096 tokens x (128 BF16 + 1 fp32) heads of 512 on one
+// than more blocks).  Where a token has few heads a block takes a run of tokens
+// instead.  4096 tokens x (128 BF16 + 1 fp32) heads of 512 on one
 // B200: 190 us, 5.75 TB/s or 0.88 of a device copy; without the loads ahead
 // 214 us at best (7 blocks), with one value at a time instead of packed fp32
 // pairs and fp64 sines 351 us.
@@ -160,6 +161,46 @@ __device__ __forceinline__ void wide_head(uint64_t (&v)[NC][4], float& r, bool w
   if (wide) r = (float)(ldexp(1.0, e) / sqrt(ldexp((double)ss / dim, 2 * e) + eps));
 }
 
+// One head as loaded: normalised, times the weight, rotated, and stored if
+// there is one.
+template <typename T, int NC, bool kVec>
+__device__ __forceinline__ void norm_head(const Raw<T> (&raw)[NC], const uint64_t (&w)[NC][4], int lph, int l, int D, int rot0,
+                                          float inv_d, float eps, double eps64, bool tiny_eps, const float2* turn, bool there,
+                                          T* y) {
+  uint64_t v[NC][4], s2 = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[c][i] = raw[c].get(i);
+      s2 = fma2(v[c][i], v[c][i], s2);
+    }
+  const float2 s = unpair(s2);
+  float ss = s.x + s.y;
+  for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  float r = __frcp_rn(sqrtf(fmaf(ss, inv_d, eps)));
+  const bool wide = !(ss <= 3.0e38f) || (tiny_eps && ss < 1e-30f);
+  if (__any_sync(0xffffffffu, wide)) wide_head<NC>(v, r, wide, lph, D, eps64);
+  const uint64_t rr = pair(r, r);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int d0 = (c * lph + l) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[c][i] = mul2(mul2(v[c][i], rr), w[c][i]);
+    if (d0 + 8 > rot0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = d0 + 2 * i;                    // D and rot0 are even: a pair never straddles
+        if (d >= rot0 && d < D) {
+          const float2 q = turn[(d - rot0) >> 1], f = unpair(v[c][i]);
+          v[c][i] = pair(fmaf(f.x, q.x, -(f.y * q.y)), fmaf(f.x, q.y, f.y * q.x));
+        }
+      }
+    }
+    if (there && d0 < D) Raw<T>::store(y + c * lph * 8, v[c], kVec ? -1 : D - d0);
+  }
+}
+
 // Heads h0 + slot, h0 + slot + slots, ... below h1 of token t.  NC: steps of
 // 8 values a lane takes; U: heads whose loads are in flight at once.  kVec:
 // 16-byte accesses.  `table`: the block's cosines and sines still have to be
@@ -217,56 +258,110 @@ __device__ __forceinline__ void norm_heads(const HeadNormArgs& a, const HeadNorm
     }
 #pragma unroll
     for (int u = 0; u < U; ++u, h += slots, y += y_step) {
-      uint64_t v[NC][4], s2 = 0;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[c][i] = raw[u][c].get(i);
-          s2 = fma2(v[c][i], v[c][i], s2);
-        }
-      const float2 s = unpair(s2);
-      float ss = s.x + s.y;
-      for (int o = lph >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      float r = __frcp_rn(sqrtf(fmaf(ss, inv_d, eps)));
-      const bool wide = !(ss <= 3.0e38f) || (tiny_eps && ss < 1e-30f);
-      if (__any_sync(0xffffffffu, wide)) wide_head<NC>(v, r, wide, lph, D, a.eps);
-      const uint64_t rr = pair(r, r);
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int d0 = (c * lph + l) * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[c][i] = mul2(mul2(v[c][i], rr), w[c][i]);
-        if (d0 + 8 > rot0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int d = d0 + 2 * i;                    // D and rot0 are even: a pair never straddles
-            if (d >= rot0 && d < D) {
-              const float2 q = cs[(d - rot0) >> 1], f = unpair(v[c][i]);
-              v[c][i] = pair(fmaf(f.x, q.x, -(f.y * q.y)), fmaf(f.x, q.y, f.y * q.x));
-            }
-          }
-        }
-        if (h < h1 && d0 < D) Raw<T>::store(y + c * lph * 8, v[c], kVec ? -1 : D - d0);
-      }
+      norm_head<T, NC, kVec>(raw[u], w, lph, l, D, rot0, inv_d, eps, a.eps, tiny_eps, cs, h < h1, y);
     }
   }
 }
 
-template <int NC>
-__device__ __forceinline__ void norm_part(const HeadNormArgs& a, const HeadNormPart& p, int64_t t, int h0, int h1,
-                                          float2* cs, bool table) {
-  // heads in flight a warp: as many as the registers hold twice
-  constexpr int U = NC == 1 ? 2 : 1;
-  if (p.f32) {
-    if (p.vec) norm_heads<float, NC, U, true>(a, p, t, h0, h1, cs, table);
-    else norm_heads<float, NC, 1, false>(a, p, t, h0, h1, cs, table);
-  } else {
-    if (p.vec) norm_heads<uint16_t, NC, NC == 4 ? 1 : 2, true>(a, p, t, h0, h1, cs, table);
-    else norm_heads<uint16_t, NC, 1, false>(a, p, t, h0, h1, cs, table);
+// Items first .. total - 1, item i being head i % heads of token t0 + i / heads,
+// the block's slots one item each at a time.  NC: steps of 8 values a lane
+// takes; U: heads whose loads are in flight at once.  kVec: 16-byte accesses.
+// `table`: the tokens' cosines and sines have to be computed (by every warp of
+// the block together).
+template <typename T, int NC, int U, bool kVec>
+__device__ __forceinline__ void norm_run(const HeadNormArgs& a, const HeadNormPart& p, int64_t t0, int first, int total,
+                                         float2* cs, bool table) {
+  const int lane = threadIdx.x & 31, lph = a.lanes, l = lane & (lph - 1);
+  const int per_warp = 32 / lph, slots = (kHnThreads / 32) * per_warp;
+  const int D = a.dim, rot0 = p.rotate ? D - a.rope : D;
+  const T* x = static_cast<const T*>(p.x) + t0 * p.x_tok + l * 8;
+  T* y = static_cast<T*>(p.y) + t0 * p.y_tok + l * 8;
+  const float inv_d = 1.f / (float)D, eps = (float)a.eps;
+  const bool tiny_eps = a.eps < 1e-20;
+  const int nh = p.heads, nt = (total + nh - 1) / nh;
+  // this lane group's item, its token and head; those of the next fetch, too
+  int item = first + (int)(threadIdx.x >> 5) * per_warp + lane / lph;
+  int tok = item / nh, h = item - tok * nh;
+  const int d_tok = slots / nh, d_h = slots - d_tok * nh;
+  int ftok = tok, fh = h;
+  uint64_t w[NC][4];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int d = (c * lph + l) * 8 + 2 * k;
+      w[c][k] = p.weight != nullptr && d < D ? pair(__ldg(p.weight + d), __ldg(p.weight + d + 1)) : pair(1.f, 1.f);
+    }
+  Raw<T> next[U][NC];
+  auto fetch = [&](int at) {                             // items at, at + slots, ...
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const T* px = x + ftok * p.x_tok + fh * p.x_head;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int left = D - (c * lph + l) * 8;
+        next[u][c].zero();
+        if (at + u * slots < total && left > 0) {
+          if (kVec) next[u][c].load(px + c * lph * 8);
+          else next[u][c].load(px + c * lph * 8, left);
+        }
+      }
+      ftok += d_tok;
+      fh += d_h;
+      if (fh >= nh) { fh -= nh; ++ftok; }
+    }
+  };
+  fetch(item);
+  for (int n = (total - first + slots * U - 1) / (slots * U); n > 0; --n) {   // the same count in every warp
+    Raw<T> raw[U][NC];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) raw[u][c] = next[u][c];
+    if (n > 1) fetch(item + U * slots);
+    if (table) {
+      table = false;
+      const int half = a.rope / 2;
+      for (int k = threadIdx.x; k < nt * half; k += kHnThreads) {
+        const int dt = k / half;
+        cs[k] = cos_sin((double)(a.positions != nullptr ? a.positions[t0 + dt] : 0) * a.theta[k - dt * half]);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      T* py = y + tok * p.y_tok + h * p.y_head;
+      // (an item beyond the last is worked on, not stored)
+      const float2* turn = cs + min(tok, nt - 1) * (a.rope / 2);
+      norm_head<T, NC, kVec>(raw[u], w, lph, l, D, rot0, inv_d, eps, a.eps, tiny_eps, turn, item < total, py);
+      item += slots;
+      tok += d_tok;
+      h += d_h;
+      if (h >= nh) { h -= nh; ++tok; }
+    }
   }
 }
 
+// kRun: items first .. end - 1 from token t on; else heads of token t.
+template <int NC, bool kRun>
+__device__ __forceinline__ void norm_part(const HeadNormArgs& a, const HeadNormPart& p, int64_t t, int first, int end,
+                                          float2* cs, bool table) {
+  // heads in flight a warp: as many as the registers hold twice
+  constexpr int U = NC == 1 ? 2 : 1, UB = NC == 4 ? 1 : 2;
+  if (p.f32) {
+    if (kRun && p.vec) norm_run<float, NC, U, true>(a, p, t, first, end, cs, table);
+    else if (kRun) norm_run<float, NC, 1, false>(a, p, t, first, end, cs, table);
+    else if (p.vec) norm_heads<float, NC, U, true>(a, p, t, first, end, cs, table);
+    else norm_heads<float, NC, 1, false>(a, p, t, first, end, cs, table);
+  } else {
+    if (kRun && p.vec) norm_run<uint16_t, NC, UB, true>(a, p, t, first, end, cs, table);
+    else if (kRun) norm_run<uint16_t, NC, 1, false>(a, p, t, first, end, cs, table);
+    else if (p.vec) norm_heads<uint16_t, NC, UB, true>(a, p, t, first, end, cs, table);
+    else norm_heads<uint16_t, NC, 1, false>(a, p, t, first, end, cs, table);
+  }
+}
+
+// A block works on some heads of one token.
 template <int NC>
 __global__ void __launch_bounds__(kHnThreads, NC == 4 ? 3 : 4) head_norm_kernel(const __grid_constant__ HeadNormArgs a) {
   __shared__ float2 cs[kHnMaxDim / 2];
@@ -278,8 +373,38 @@ __global__ void __launch_bounds__(kHnThreads, NC == 4 ? 3 : 4) head_norm_kernel(
   const int qb = b - q.block0, kb = b - k.block0;
   const bool has_q = qb >= 0 && qb < q.blocks, has_k = kb >= 0 && kb < k.blocks;
   const bool table = (has_q && q.rotate) || (has_k && k.rotate);
-  if (has_q) norm_part<NC>(a, q, t, qb * q.block_heads, min(q.heads, (qb + 1) * q.block_heads), cs, table);
-  if (has_k) norm_part<NC>(a, k, t, kb * k.block_heads, min(k.heads, (kb + 1) * k.block_heads), cs, table && !has_q);
+  if (has_q) norm_part<NC, false>(a, q, t, qb * q.block_heads, min(q.heads, (qb + 1) * q.block_heads), cs, table);
+  if (has_k) norm_part<NC, false>(a, k, t, kb * k.block_heads, min(k.heads, (kb + 1) * k.block_heads), cs, table && !has_q);
+}
+
+// A block works on a run of tokens' heads.  The queries' heads and then the
+// keys', token by token, are one list in which a head costs its values' bytes;
+// a block takes `share` of the list's cost, from each part the tokens whose
+// sines fit at a time.
+template <int NC>
+__global__ void __launch_bounds__(kHnThreads, NC == 4 ? 3 : 4) head_norm_run_kernel(const __grid_constant__ HeadNormArgs a) {
+  __shared__ float2 cs[kHnMaxDim / 2];
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
+  const int64_t lo = blockIdx.x * a.share, hi = lo + a.share;
+  int64_t before = 0;                                    // the cost of the parts ahead
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const HeadNormPart& p = a.part[s];
+    const int lg = p.f32 ? 1 : 0;
+    const int64_t cost = (a.n_tok * p.heads) << lg;
+    auto item = [&](int64_t c) { return (min(max(c - before, (int64_t)0), cost) + lg) >> lg; };
+    const int64_t i0 = item(lo), i1 = item(hi);
+    if (i0 < i1) {
+      for (int64_t t = i0 / p.heads; t * p.heads < i1; t += a.group) {
+        __syncthreads();                                 // the sines of the tokens before are read no more
+        const int64_t base = t * p.heads;
+        norm_part<NC, true>(a, p, t, (int)max(i0 - base, (int64_t)0), (int)min(i1 - base, (int64_t)a.group * p.heads), cs,
+                            p.rotate);
+      }
+    }
+    before += cost;
+  }
 }
 
 }  // namespace
@@ -297,7 +422,7 @@ cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st) {
   // fewer tokens the heads are spread over blocks of at least one pass, the
   // keys in blocks of their own.
   const int64_t want = (8LL * sms + a.n_tok - 1) / a.n_tok;
-  int64_t blocks = 0;
+  int64_t blocks = 0, items = 0, cost = 0;
   for (HeadNormPart& p : a.part) {
     if (p.heads == 0) { p.blocks = p.block0 = 0; p.block_heads = 1; continue; }
     const int al = p.f32 ? 4 : 8;
@@ -309,11 +434,24 @@ cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st) {
     p.blocks = (int)((p.heads + bh - 1) / bh);
     p.block0 = want == 1 ? 0 : (int)blocks;
     blocks = std::max<int64_t>(blocks, p.block0 + p.blocks);
+    items += a.n_tok * p.heads;
+    cost += (a.n_tok * p.heads) << (p.f32 ? 1 : 0);
   }
   a.blocks = (int)blocks;
-  const int64_t grid = blocks * a.n_tok;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  int64_t grid = blocks * a.n_tok;
   if (grid == 0) return cudaSuccess;
+  // Tokens of few heads would leave such a block after a pass or two, before
+  // its loads ahead gain anything: one wave of blocks with runs of tokens.
+  // (4040 tokens x 11 heads of 384: 30 us instead of 41; 700 x 9 of 1024: 9.2
+  // instead of 17; but 2048 x 72 of 128, nine passes: 33 instead of 31.)
+  const int64_t wave = (nc == 4 ? 3LL : 4LL) * sms;
+  const bool run = a.part[0].heads + a.part[1].heads <= 4 * slots && items > 2 * wave * slots;
+  if (run) {
+    a.share = (cost + wave - 1) / wave;
+    grid = (cost + a.share - 1) / a.share;
+    a.group = a.rope ? kHnMaxDim / a.rope : kHnMaxDim;
+  }
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3((unsigned)grid);
   lc.blockDim = dim3(kHnThreads);
@@ -323,7 +461,8 @@ cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&lc, nc == 1 ? head_norm_kernel<1> : nc == 2 ? head_norm_kernel<2> : head_norm_kernel<4>, a);
+  cudaError_t e = run ? cudaLaunchKernelEx(&lc, nc == 1 ? head_norm_run_kernel<1> : nc == 2 ? head_norm_run_kernel<2> : head_norm_run_kernel<4>, a)
+                      : cudaLaunchKernelEx(&lc, nc == 1 ? head_norm_kernel<1> : nc == 2 ? head_norm_kernel<2> : head_norm_kernel<4>, a);
   note_launch();
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

@@ -20,6 +20,8 @@ struct HeadNormArgs {
   double eps;
   int dim, rope;
   int lanes, blocks;                   // lanes of a head, blocks of a token (set by the launch)
+  int group;                           // for blocks with runs of tokens, set by the launch: the tokens whose sines are
+  int64_t share;                       // kept at once, and the cost a block takes
   HeadNormPart part[2];
 };
 

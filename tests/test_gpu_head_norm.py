@@ -91,6 +91,14 @@ def test_matches_the_oracle(n, H, HK, D, R, qt, kt, rot):
     _check(ko[:n], k, kw, 1e-6, pos if rot else None, R, "k")
 
 
+@pytest.mark.parametrize("n,H,HK,D,R,qt,kt,rot", [
+    (1501, 4, 7, 384, 86, BF, BF, True), (517, 28, 4, 288, 64, F32, F32, True), (700, 3, 1, 1024, 1024, BF, F32, True),
+    (2049, 1, 2, 16, 16, F32, BF, False), (40, 200, 1, 520, 6, BF, BF, True), (5, 1000, 3, 256, 0, BF, F32, False)])
+def test_many_tokens_of_few_heads(n, H, HK, D, R, qt, kt, rot):
+    """A block's run of heads crosses tokens, and goes from queries to keys."""
+    test_matches_the_oracle(n, H, HK, D, R, qt, kt, rot)
+
+
 @pytest.mark.parametrize("D", [64, 512])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_strides_offsets_and_in_place(D, dtype):
