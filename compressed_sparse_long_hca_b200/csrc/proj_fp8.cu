@@ -697,6 +697,58 @@ int fp8_splits(int row_tiles, int k_blocks, int sms) {
   return s;
 }
 
+// The form of more than 64 tokens: pairs of SMs, whole tiles of one SM or a
+// CTA per part of a tile, and the tokens of a tile.  Each has an estimated time,
+// waves x (K blocks x time of a block + time of a tile's end), and the least is
+// taken; the constants (microseconds) are fits to measured calls:
+//   639 x 750 x 8496      whole, 32 tokens a tile 22.3   parts, 128 tokens 17.0
+//   140 x 1624 x 5320     whole, 80 tokens 16.4          parts, 96 tokens 11.3
+//   905 x 89 x 12512      whole, 32 tokens 30.0          parts, 64 tokens 15.4
+//   128 x 9000 x 2048     parts, 128 tokens 15.6         whole, 64 tokens 9.5
+//   160 x 7168 x 16384    pairs 41.9                     whole, 80 tokens 36.9
+//   256 x 24576 x 1536    whole, 128 tokens 17.1         pairs 15.2
+//   2754 x 2564 x 488     pairs 16.2                     whole, 128 tokens 15.4
+// A pair stores output rows that are not on 32 bytes more slowly; the plan,
+// which does not know the outputs, takes the row length for that.
+void choose_form(Plan& p, int n_out, int groups, int n_tok, int sms) {
+  double best = 1e30;
+  const int t16 = (n_tok + 15) / 16;
+  auto waves = [](int64_t n, int at_once) { return (double)((n + at_once - 1) / at_once); };
+  for (int most = 128; most >= 32; most -= 16) {
+    const int tok_tiles = (16 * t16 + most - 1) / most;
+    const int tile_n = (t16 + tok_tiles - 1) / tok_tiles * 16;
+    const int64_t tiles = (int64_t)p.row_tiles * ((n_tok + tile_n - 1) / tile_n);
+    const double block = 0.215 + 0.0004 * tile_n;
+    for (int spread = 0; spread <= (p.splits > 1 ? 1 : 0); ++spread) {
+      double cost;
+      if (spread) {
+        // two CTAs share an SM (clusters fill 7/8 of the places)
+        const int64_t ctas = tiles * p.splits;
+        cost = waves(8 * ctas, 14 * sms) * ((ctas > sms ? 2.0 : 1.0) * p.k_blocks / p.splits * block + 2.3 + 0.02 * tile_n);
+      } else {
+        cost = waves(tiles, sms) * (p.k_blocks * block + 0.4 + 0.01 * tile_n);
+      }
+      if (cost < best && tiles <= 0x7FFFFFFF / kMaxParts) {
+        best = cost;
+        p.nt = 128;
+        p.tile_n = tile_n;
+        p.tok_tiles = (n_tok + tile_n - 1) / tile_n;
+        p.spread = spread;
+      }
+    }
+  }
+  if (n_tok <= kRowTile) return;
+  const int m_tiles = (n_tok + 2 * kRowTile - 1) / (2 * kRowTile), f_tiles = pair_tiles(n_out / groups);
+  const int tile_f = pair_features(n_out / groups);
+  const double end = (n_out % 16 == 0 ? 0.009 : 0.024) * tile_f;
+  if (waves((int64_t)groups * f_tiles * m_tiles, sms / 2) * (p.k_blocks * (0.13 + 0.0007 * tile_f) + end) < best) {
+    p.pair = true;
+    p.spread = false;
+    p.nt = p.tile_n = kRowTile;
+    p.tok_tiles = 2 * m_tiles;
+  }
+}
+
 Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
   Plan p{};
   p.row_tiles = (n_out + kRowTile - 1) / kRowTile;
@@ -707,34 +759,19 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
   if (p.fuse) {
     p.nt = p.tile_n = kFuseTokens;
     p.tok_tiles = 1;
+    p.spread = p.splits > 1;
   } else {
-    // pairs of SMs beyond 128 tokens, unless their tiles of 256 tokens are so
-    // few that single SMs finish first (512 tokens x 2368 features: 22 pairs
-    // and 133 SMs take the same time)
-    const int m_tiles = (n_tok + 2 * kRowTile - 1) / (2 * kRowTile);
-    const int64_t pairs = (int64_t)groups * pair_tiles(n_out / groups) * m_tiles;
-    p.pair = n_tok > kRowTile && 6 * pairs > sms;
-    if (p.pair) {
-      p.nt = p.tile_n = kRowTile;
-      p.tok_tiles = 2 * m_tiles;
-    } else if (n_tok <= 64) {
+    if (n_tok <= 64) {
       p.nt = n_tok <= 32 ? 32 : 64;
       p.tok_tiles = 1;
       p.tile_n = (n_tok + 15) / 16 * 16;
+      p.spread = p.splits > 1 && 2 * p.row_tiles <= sms;
     } else {
-      // token tiles of at most 128: as many as the SMs take at once
-      p.nt = 128;
-      p.tok_tiles = (n_tok + p.nt - 1) / p.nt;
-      const int most = std::min(sms / p.row_tiles, (n_tok + 31) / 32);
-      if (p.tok_tiles < most && n_tok > p.nt) p.tok_tiles = most;
-      p.tile_n = ((n_tok + p.tok_tiles - 1) / p.tok_tiles + 15) / 16 * 16;
-      p.tok_tiles = (n_tok + p.tile_n - 1) / p.tile_n;
+      choose_form(p, n_out, groups, n_tok, sms);
     }
   }
   p.chunks = (p.tile_n + 127) / 128;
   p.tiles = p.row_tiles * p.tok_tiles;
-  // one CTA per part where whole tiles would leave half of the SMs idle
-  p.spread = p.splits > 1 && !p.pair && (p.fuse || 2 * p.tiles <= sms);
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   if (!p.fuse) {
     p.xp = 0;

@@ -284,8 +284,43 @@ def test_refusals():
         quantize_fp8_weight(torch.zeros((8, 12), device="cuda"))
 
 
+# n_out, k_in, groups, n_tok
+FORMS = [
+    (257, 2056, 1, 130),          # a CTA per part: five token tiles of 32
+    (750, 8496, 1, 639),          # a CTA per part: five of 128
+    (2051, 8200, 1, 130),         # a CTA per part: more clusters than the SMs hold at once
+    (107, 2022 * 8, 1, 1030),     # one row tile, eight parts, 64 tokens a tile
+    (2022, 680, 1, 107),          # whole tiles of at most 128 tokens, four of 32
+    (8001, 264, 1, 1000),         # whole tiles, several per SM
+    (8001, 1032, 1, 450),         # pairs, output rows of odd length
+    (6400, 10 * 528, 10, 780),    # pairs, grouped: feature tiles that begin inside a row tile
+    (9456, 1160, 1, 513),         # pairs: two K parts, a ragged last tile, one token beyond two tiles
+]
+
+
+@pytest.mark.parametrize("n_out,k_in,groups,n_tok", FORMS)
+def test_every_form_of_many_tokens(n_out, k_in, groups, n_tok):
+    """Against the oracle, in both types; the first tokens alone, which another
+    form computes, have the same bits; rows behind the last stay as they were."""
+    x, _, codes, scales = _inputs(n_out, k_in, groups, n_tok, n_tok)
+    lin, xd = _linear(codes, scales, groups), x.cuda()
+    y = torch.full((n_tok + 1, n_out), 7.0, device="cuda")
+    lin(xd, y[:n_tok])
+    pick = np.unique(np.r_[0:8, n_tok // 2, n_tok - 40:n_tok])         # the oracle's share of the tokens
+    _check(y[pick], x[pick], codes, scales, groups)
+    b = torch.full((n_tok + 1, n_out), 7.0, device="cuda", dtype=torch.bfloat16)
+    lin(xd, b[:n_tok])
+    assert torch.equal(b[:n_tok], y[:n_tok].to(torch.bfloat16))
+    assert bool((y[n_tok] == 7).all()) and bool((b[n_tok] == 7).all())
+    few = torch.empty((50, n_out), device="cuda")
+    lin(xd[:50], few)
+    assert torch.equal(few, y[:50])
+    from compressed_sparse_long_hca_b200.api import LinearFP8
+    LinearFP8.check_device_error()
+
+
 @pytest.mark.parametrize("n_out,k_in,n_tok", [(2368, 1536, 6), (2368, 1536, 50), (2368, 1536, 100), (700, 300 * 8, 300), (20001, 264, 300),
-                                              (9100, 1160, 513)])
+                                              (9100, 1160, 513), (8001, 1032, 450), (9456, 1160, 513), (750, 8496, 639)])
 def test_segments_that_begin_anywhere(n_out, k_in, n_tok):
     """Segments of odd sizes, in every form of the launch: the outputs are
     those of one segment, and nothing beside them is written."""
