@@ -683,8 +683,10 @@ namespace {
 struct Plan {
   int row_tiles, k_blocks, sup, splits, nt, tok_tiles, tile_n, chunks, tiles;
   bool fuse, spread, pair;
-  size_t xp, xsf, total;      // workspace offsets and size
+  size_t xsf;                 // workspace offset of the tokens' scales (their codes come first)
 };
+
+size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 // K parts of a weight: a function of its shape and the device alone.  The
 // power of two that gives the SMs two CTAs each, every part at least
@@ -772,12 +774,7 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
   }
   p.chunks = (p.tile_n + 127) / 128;
   p.tiles = p.row_tiles * p.tok_tiles;
-  auto al = [](size_t x) { return (x + 255) / 256 * 256; };
-  if (!p.fuse) {
-    p.xp = 0;
-    p.xsf = al((size_t)groups * p.k_blocks * p.tok_tiles * p.tile_n * kKBlk);
-    p.total = p.xsf + al((size_t)groups * p.sup * p.tok_tiles * p.chunks * kSfBytes);
-  }
+  p.xsf = al256((size_t)groups * p.k_blocks * p.tok_tiles * p.tile_n * kKBlk);
   return p;
 }
 
@@ -842,8 +839,14 @@ WeightLayout weight_layout(int n_out, int k_in, int groups) {
 
 size_t fp8_weight_bytes(int n_out, int k_in, int groups) { return weight_layout(n_out, k_in, groups).total; }
 
-size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok, int sms) {
-  return fp8_plan(n_out, k_in, groups, n_tok, sms).total;
+// Room for the quantised tokens in every form of n_tok tokens, so that a
+// workspace for many tokens serves fewer, too: a form's last tile reaches at
+// most 255 rows beyond the tokens, and beyond 64 tokens tiles have at least 32.
+size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok) {
+  if (n_tok <= kFuseTokens) return 0;
+  const size_t k_blocks = (k_in / groups + kKBlk - 1) / kKBlk, sup = (k_blocks + 3) / 4;
+  const size_t rows = n_tok <= 64 ? (n_tok + 15) / 16 * 16 : n_tok + 255, tiles = n_tok <= 64 ? 1 : (n_tok + 31) / 32;
+  return al256(groups * k_blocks * rows * kKBlk) + al256(groups * sup * tiles * kSfBytes);
 }
 
 cudaError_t launch_fp8_pack_weight(const uint8_t* codes, const uint8_t* scales, int n_out, int k_in, int groups,
@@ -906,7 +909,7 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
     a.quant_groups = (p.spread ? p.k_blocks / p.splits : p.k_blocks) >= 16 ? 2 : 1;
     return launch_nt<kFuseTokens, true, false>(a, sms, st);
   }
-  a.xp = base + p.xp;
+  a.xp = base;
   a.xsf = base + p.xsf;
   // (An ordinary launch: with programmatic serialization its blocks were
   // resident, waiting, beside the kernel ahead, and 512 tokens x 2368 x 4096
@@ -918,7 +921,7 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   lc.blockDim = dim3(256);
   lc.stream = st;
   cudaError_t e = cudaLaunchKernelEx(&lc, fp8_quant_x_kernel, x, n_tok, kg, (int64_t)k_in, p.k_blocks, p.sup, p.tok_tiles,
-                                     p.tile_n, p.chunks, aligned, base + p.xp, base + p.xsf);
+                                     p.tile_n, p.chunks, aligned, base, base + p.xsf);
   note_launch();
   if (e != cudaSuccess) return e;
   if (p.pair) {

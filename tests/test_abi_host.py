@@ -237,3 +237,11 @@ def test_head_norm_argument_errors_on_the_host(cuda_lib):
         assert msg in cuda_lib.csa_last_error(), (args, cuda_lib.csa_last_error())
     assert f(0, 64, 16, 1e-6, None, None, q, None, None) == 0              # no tokens: nothing to do
     assert f(4, 64, 16, 1e-6, None, None, part(heads=0), None, None) == 0  # no heads
+
+
+def test_an_fp8_workspace_serves_every_smaller_call(cuda_lib):
+    for n_out, k_in, groups in ((33, 64, 1), (750, 8496, 1), (8001, 1032, 1), (2048, 4096, 16)):
+        sizes = [cuda_lib.csa_gemm_fp8_workspace_bytes(n_out, k_in, groups, n) for n in range(1, 1400)]
+        assert sizes[:16] == [0] * 16
+        assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+        assert all(s >= n * k_in for n, s in enumerate(sizes, 1) if n > 16)

@@ -315,6 +315,11 @@ def test_every_form_of_many_tokens(n_out, k_in, groups, n_tok):
     few = torch.empty((50, n_out), device="cuda")
     lin(xd[:50], few)
     assert torch.equal(few, y[:50])
+    need = lin.workspace_bytes(n_tok)                                  # the call stays within its workspace
+    ws = torch.full((need + 4096,), 90, dtype=torch.uint8, device="cuda")
+    b.zero_()
+    lin(xd, b[:n_tok], workspace=ws[:need])
+    assert torch.equal(b[:n_tok], y[:n_tok].to(torch.bfloat16)) and bool((ws[need:] == 90).all())
     from compressed_sparse_long_hca_b200.api import LinearFP8
     LinearFP8.check_device_error()
 
