@@ -13,8 +13,8 @@
 // shadow of the loads, and every further head reuses them; the next heads'
 // loads are issued before the present ones are worked on (4 blocks of 128
 // threads an SM: the registers that the loads in flight take are worth more
-// than more blocks).  Where a token has few heads a block takes a run of tokens
-// instead.  4096 tokens x (128 BF16 + 1 fp32) heads of 512 on one
+// than more blocks).  Where many tokens have few heads each, a block takes a
+// run of tokens instead.  4096 tokens x (128 BF16 + 1 fp32) heads of 512 on one
 // B200: 190 us, 5.75 TB/s or 0.88 of a device copy; without the loads ahead
 // 214 us at best (7 blocks), with one value at a time instead of packed fp32
 // pairs and fp64 sines 351 us.
@@ -258,7 +258,8 @@ __device__ __forceinline__ void norm_heads(const HeadNormArgs& a, const HeadNorm
     }
 #pragma unroll
     for (int u = 0; u < U; ++u, h += slots, y += y_step) {
-      norm_head<T, NC, kVec>(raw[u], w, lph, l, D, rot0, inv_d, eps, a.eps, tiny_eps, cs, h < h1, y);
+      if (u == 0 || __any_sync(0xffffffffu, h < h1))
+        norm_head<T, NC, kVec>(raw[u], w, lph, l, D, rot0, inv_d, eps, a.eps, tiny_eps, cs, h < h1, y);
     }
   }
 }
@@ -266,10 +267,10 @@ __device__ __forceinline__ void norm_heads(const HeadNormArgs& a, const HeadNorm
 // Items first .. total - 1, item i being head i % heads of token t0 + i / heads,
 // the block's slots one item each at a time.  NC: steps of 8 values a lane
 // takes; U: heads whose loads are in flight at once.  kVec: 16-byte accesses.
-// `table`: the tokens' cosines and sines have to be computed (by every warp of
-// the block together).
+// `table`: the cosines and sines of tokens t0 .. t0 + nt - 1 have to be computed
+// (by every warp of the block together).
 template <typename T, int NC, int U, bool kVec>
-__device__ __forceinline__ void norm_run(const HeadNormArgs& a, const HeadNormPart& p, int64_t t0, int first, int total,
+__device__ __forceinline__ void norm_run(const HeadNormArgs& a, const HeadNormPart& p, int64_t t0, int nt, int first, int total,
                                          float2* cs, bool table) {
   const int lane = threadIdx.x & 31, lph = a.lanes, l = lane & (lph - 1);
   const int per_warp = 32 / lph, slots = (kHnThreads / 32) * per_warp;
@@ -278,7 +279,7 @@ __device__ __forceinline__ void norm_run(const HeadNormArgs& a, const HeadNormPa
   T* y = static_cast<T*>(p.y) + t0 * p.y_tok + l * 8;
   const float inv_d = 1.f / (float)D, eps = (float)a.eps;
   const bool tiny_eps = a.eps < 1e-20;
-  const int nh = p.heads, nt = (total + nh - 1) / nh;
+  const int nh = p.heads;
   // this lane group's item, its token and head; those of the next fetch, too
   int item = first + (int)(threadIdx.x >> 5) * per_warp + lane / lph;
   int tok = item / nh, h = item - tok * nh;
@@ -333,7 +334,8 @@ __device__ __forceinline__ void norm_run(const HeadNormArgs& a, const HeadNormPa
       T* py = y + tok * p.y_tok + h * p.y_head;
       // (an item beyond the last is worked on, not stored)
       const float2* turn = cs + min(tok, nt - 1) * (a.rope / 2);
-      norm_head<T, NC, kVec>(raw[u], w, lph, l, D, rot0, inv_d, eps, a.eps, tiny_eps, turn, item < total, py);
+      if (u == 0 || __any_sync(0xffffffffu, item < total))
+        norm_head<T, NC, kVec>(raw[u], w, lph, l, D, rot0, inv_d, eps, a.eps, tiny_eps, turn, item < total, py);
       item += slots;
       tok += d_tok;
       h += d_h;
@@ -344,26 +346,26 @@ __device__ __forceinline__ void norm_run(const HeadNormArgs& a, const HeadNormPa
 
 // kRun: items first .. end - 1 from token t on; else heads of token t.
 template <int NC, bool kRun>
-__device__ __forceinline__ void norm_part(const HeadNormArgs& a, const HeadNormPart& p, int64_t t, int first, int end,
+__device__ __forceinline__ void norm_part(const HeadNormArgs& a, const HeadNormPart& p, int64_t t, int nt, int first, int end,
                                           float2* cs, bool table) {
   // heads in flight a warp: as many as the registers hold twice
   constexpr int U = NC == 1 ? 2 : 1, UB = NC == 4 ? 1 : 2;
   if (p.f32) {
-    if (kRun && p.vec) norm_run<float, NC, U, true>(a, p, t, first, end, cs, table);
-    else if (kRun) norm_run<float, NC, 1, false>(a, p, t, first, end, cs, table);
+    if (kRun && p.vec) norm_run<float, NC, U, true>(a, p, t, nt, first, end, cs, table);
+    else if (kRun) norm_run<float, NC, 1, false>(a, p, t, nt, first, end, cs, table);
     else if (p.vec) norm_heads<float, NC, U, true>(a, p, t, first, end, cs, table);
     else norm_heads<float, NC, 1, false>(a, p, t, first, end, cs, table);
   } else {
-    if (kRun && p.vec) norm_run<uint16_t, NC, UB, true>(a, p, t, first, end, cs, table);
-    else if (kRun) norm_run<uint16_t, NC, 1, false>(a, p, t, first, end, cs, table);
+    if (kRun && p.vec) norm_run<uint16_t, NC, UB, true>(a, p, t, nt, first, end, cs, table);
+    else if (kRun) norm_run<uint16_t, NC, 1, false>(a, p, t, nt, first, end, cs, table);
     else if (p.vec) norm_heads<uint16_t, NC, UB, true>(a, p, t, first, end, cs, table);
     else norm_heads<uint16_t, NC, 1, false>(a, p, t, first, end, cs, table);
   }
 }
 
-// A block works on some heads of one token.
-template <int NC>
-__global__ void __launch_bounds__(kHnThreads, NC == 4 ? 3 : 4) head_norm_kernel(const __grid_constant__ HeadNormArgs a) {
+// A block works on some heads of one token.  kPerSm: blocks an SM holds.
+template <int NC, int kPerSm>
+__global__ void __launch_bounds__(kHnThreads, kPerSm) head_norm_kernel(const __grid_constant__ HeadNormArgs a) {
   __shared__ float2 cs[kHnMaxDim / 2];
   tc::griddep_launch_dependents();
   tc::griddep_wait();
@@ -373,37 +375,37 @@ __global__ void __launch_bounds__(kHnThreads, NC == 4 ? 3 : 4) head_norm_kernel(
   const int qb = b - q.block0, kb = b - k.block0;
   const bool has_q = qb >= 0 && qb < q.blocks, has_k = kb >= 0 && kb < k.blocks;
   const bool table = (has_q && q.rotate) || (has_k && k.rotate);
-  if (has_q) norm_part<NC, false>(a, q, t, qb * q.block_heads, min(q.heads, (qb + 1) * q.block_heads), cs, table);
-  if (has_k) norm_part<NC, false>(a, k, t, kb * k.block_heads, min(k.heads, (kb + 1) * k.block_heads), cs, table && !has_q);
+  if (has_q) norm_part<NC, false>(a, q, t, 1, qb * q.block_heads, min(q.heads, (qb + 1) * q.block_heads), cs, table);
+  if (has_k) norm_part<NC, false>(a, k, t, 1, kb * k.block_heads, min(k.heads, (kb + 1) * k.block_heads), cs, table && !has_q);
 }
 
-// A block works on a run of tokens' heads.  The queries' heads and then the
-// keys', token by token, are one list in which a head costs its values' bytes;
-// a block takes `share` of the list's cost, from each part the tokens whose
-// sines fit at a time.
+// A block works on a run of tokens.  The heads of all tokens, a token's queries
+// before its keys, are one list in which a head costs its values' bytes; a
+// block takes `share` of the list's cost.  The tokens whose sines fit are done
+// at a time, their queries and then their keys.
 template <int NC>
 __global__ void __launch_bounds__(kHnThreads, NC == 4 ? 3 : 4) head_norm_run_kernel(const __grid_constant__ HeadNormArgs a) {
   __shared__ float2 cs[kHnMaxDim / 2];
   tc::griddep_launch_dependents();
   tc::griddep_wait();
-  const int64_t lo = blockIdx.x * a.share, hi = lo + a.share;
-  int64_t before = 0;                                    // the cost of the parts ahead
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const HeadNormPart& p = a.part[s];
-    const int lg = p.f32 ? 1 : 0;
-    const int64_t cost = (a.n_tok * p.heads) << lg;
-    auto item = [&](int64_t c) { return (min(max(c - before, (int64_t)0), cost) + lg) >> lg; };
-    const int64_t i0 = item(lo), i1 = item(hi);
-    if (i0 < i1) {
-      for (int64_t t = i0 / p.heads; t * p.heads < i1; t += a.group) {
-        __syncthreads();                                 // the sines of the tokens before are read no more
-        const int64_t base = t * p.heads;
-        norm_part<NC, true>(a, p, t, (int)max(i0 - base, (int64_t)0), (int)min(i1 - base, (int64_t)a.group * p.heads), cs,
-                            p.rotate);
-      }
-    }
-    before += cost;
+  const HeadNormPart &q = a.part[0], &k = a.part[1];
+  const int lq = q.f32 ? 1 : 0, lk = k.f32 ? 1 : 0, cq = q.heads << lq, c = cq + (k.heads << lk);
+  const int64_t lo = blockIdx.x * a.share, hi = min(lo + a.share, a.n_tok * c);
+  auto token = [&](int64_t v) { return v <= 0x7FFFFFFF ? (int64_t)((uint32_t)v / (uint32_t)c) : v / c; };
+  // the first query and key heads of a token that lie at its cost `v` or behind
+  auto q_head = [&](int v) { return min(q.heads, (v + lq) >> lq); };
+  auto k_head = [&](int v) { return min(k.heads, (max(v - cq, 0) + lk) >> lk); };
+  const int64_t ta = token(lo), tb = token(hi);          // the first token, and the one at which the run ends
+  const int va = (int)(lo - ta * c), vb = (int)(hi - tb * c);
+  for (int64_t t = ta; t < tb + (vb > 0); t += a.group) {
+    if (t > ta) __syncthreads();                         // the sines of the tokens before are read no more
+    const int nt = (int)min(tb + (vb > 0) - t, (int64_t)a.group);
+    const bool last = tb - t < a.group;
+    const int full = last ? (int)(tb - t) : nt;          // tokens that are not cut at their end
+    const int q0 = t == ta ? q_head(va) : 0, q1 = full * q.heads + (last ? q_head(vb) : 0);
+    const int k0 = t == ta ? k_head(va) : 0, k1 = full * k.heads + (last ? k_head(vb) : 0);
+    if (q0 < q1) norm_part<NC, true>(a, q, t, nt, q0, q1, cs, q.rotate);
+    if (k0 < k1) norm_part<NC, true>(a, k, t, nt, k0, k1, cs, k.rotate && !(q0 < q1 && q.rotate));
   }
 }
 
@@ -422,7 +424,7 @@ cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st) {
   // fewer tokens the heads are spread over blocks of at least one pass, the
   // keys in blocks of their own.
   const int64_t want = (8LL * sms + a.n_tok - 1) / a.n_tok;
-  int64_t blocks = 0, items = 0, cost = 0;
+  int64_t blocks = 0, cost = 0;
   for (HeadNormPart& p : a.part) {
     if (p.heads == 0) { p.blocks = p.block0 = 0; p.block_heads = 1; continue; }
     const int al = p.f32 ? 4 : 8;
@@ -434,18 +436,22 @@ cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st) {
     p.blocks = (int)((p.heads + bh - 1) / bh);
     p.block0 = want == 1 ? 0 : (int)blocks;
     blocks = std::max<int64_t>(blocks, p.block0 + p.blocks);
-    items += a.n_tok * p.heads;
     cost += (a.n_tok * p.heads) << (p.f32 ? 1 : 0);
   }
   a.blocks = (int)blocks;
   int64_t grid = blocks * a.n_tok;
   if (grid == 0) return cudaSuccess;
-  // Tokens of few heads would leave such a block after a pass or two, before
-  // its loads ahead gain anything: one wave of blocks with runs of tokens.
-  // (4040 tokens x 11 heads of 384: 30 us instead of 41; 700 x 9 of 1024: 9.2
-  // instead of 17; but 2048 x 72 of 128, nine passes: 33 instead of 31.)
+  // Beyond two waves of such blocks, tokens of few heads leave them after a
+  // pass or two, before their loads ahead gain anything: one wave of blocks
+  // with runs of tokens then.  (4000 tokens x 3 heads of 64, one pass: 5.2 us
+  // instead of 20; 3000 x 26 of 128, 4 passes: 18 instead of 27; 1000 x 40 BF16
+  // heads of 256, 10 passes: 18 instead of 23; but 2048 x 72 heads of 128, 9
+  // passes: BF16 29 instead of 25, fp32 49 instead of 41; and in less than two
+  // waves, 500 x 3 of 64: 4.8 instead of 4.2.)
   const int64_t wave = (nc == 4 ? 3LL : 4LL) * sms;
-  const bool run = a.part[0].heads + a.part[1].heads <= 4 * slots && items > 2 * wave * slots;
+  const bool many = grid > 2 * wave;
+  const int passes = (a.part[0].heads + a.part[1].heads + slots - 1) / slots;
+  const bool run = many && passes <= (nc == 2 && !a.part[a.part[0].heads ? 0 : 1].f32 ? 10 : 6);
   if (run) {
     a.share = (cost + wave - 1) / wave;
     grid = (cost + a.share - 1) / a.share;
@@ -461,8 +467,13 @@ cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
   lc.numAttrs = 1;
-  cudaError_t e = run ? cudaLaunchKernelEx(&lc, nc == 1 ? head_norm_run_kernel<1> : nc == 2 ? head_norm_run_kernel<2> : head_norm_run_kernel<4>, a)
-                      : cudaLaunchKernelEx(&lc, nc == 1 ? head_norm_kernel<1> : nc == 2 ? head_norm_kernel<2> : head_norm_kernel<4>, a);
+  // (Short heads take six blocks an SM where there are many: 2048 tokens x 72
+  // BF16 heads of 128 25 us instead of 29; few blocks do better with four, 130
+  // x 27 of 96 2.6 instead of 3.0.)
+  void (*kernel)(HeadNormArgs) = nc == 1 ? (many ? head_norm_kernel<1, 6> : head_norm_kernel<1, 4>)
+                                 : nc == 2 ? head_norm_kernel<2, 4> : head_norm_kernel<4, 3>;
+  if (run) kernel = nc == 1 ? head_norm_run_kernel<1> : nc == 2 ? head_norm_run_kernel<2> : head_norm_run_kernel<4>;
+  cudaError_t e = cudaLaunchKernelEx(&lc, kernel, a);
   note_launch();
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

@@ -93,7 +93,9 @@ def test_matches_the_oracle(n, H, HK, D, R, qt, kt, rot):
 
 @pytest.mark.parametrize("n,H,HK,D,R,qt,kt,rot", [
     (1501, 4, 7, 384, 86, BF, BF, True), (517, 28, 4, 288, 64, F32, F32, True), (700, 3, 1, 1024, 1024, BF, F32, True),
-    (2049, 1, 2, 16, 16, F32, BF, False), (40, 200, 1, 520, 6, BF, BF, True), (5, 1000, 3, 256, 0, BF, F32, False)])
+    (2049, 1, 2, 16, 16, F32, BF, False), (40, 200, 1, 520, 6, BF, BF, True), (5, 1000, 3, 256, 0, BF, F32, False),
+    (1300, 5, 3, 128, 64, BF, F32, True), (1300, 0, 3, 100, 10, BF, F32, True), (1300, 2, 0, 70, 70, F32, BF, False),
+    (2500, 72, 8, 64, 2, F32, BF, True), (3000, 1, 1, 1024, 2, BF, BF, False), (1200, 90, 2, 128, 64, BF, BF, False)])
 def test_many_tokens_of_few_heads(n, H, HK, D, R, qt, kt, rot):
     """A block's run of heads crosses tokens, and goes from queries to keys."""
     test_matches_the_oracle(n, H, HK, D, R, qt, kt, rot)
