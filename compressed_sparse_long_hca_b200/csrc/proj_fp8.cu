@@ -709,9 +709,11 @@ int fp8_splits(int row_tiles, int k_blocks, int sms) {
 //   128 x 9000 x 2048     parts, 128 tokens 15.6         whole, 64 tokens 9.5
 //   160 x 7168 x 16384    pairs 41.9                     whole, 80 tokens 36.9
 //   256 x 24576 x 1536    whole, 128 tokens 17.1         pairs 15.2
-//   2754 x 2564 x 488     pairs 16.2                     whole, 128 tokens 15.4
-// A pair stores output rows that are not on 32 bytes more slowly; the plan,
-// which does not know the outputs, takes the row length for that.
+//   2754 x 2564 x 488     whole, 128 tokens 15.5         pairs 12.7
+//   595 x 8875 x 1224     pairs 21.9                     whole, 128 tokens 15.4
+// A pair stores output rows that are not on 32 bytes more slowly, and odd ones
+// more slowly still; the plan, which does not know the outputs, takes the row
+// length for that.
 void choose_form(Plan& p, int n_out, int groups, int n_tok, int sms) {
   double best = 1e30;
   const int t16 = (n_tok + 15) / 16;
@@ -742,7 +744,7 @@ void choose_form(Plan& p, int n_out, int groups, int n_tok, int sms) {
   if (n_tok <= kRowTile) return;
   const int m_tiles = (n_tok + 2 * kRowTile - 1) / (2 * kRowTile), f_tiles = pair_tiles(n_out / groups);
   const int tile_f = pair_features(n_out / groups);
-  const double end = (n_out % 16 == 0 ? 0.009 : 0.024) * tile_f;
+  const double end = (n_out % 16 == 0 ? 0.009 : n_out % 2 == 0 ? 0.017 : 0.024) * tile_f;
   if (waves((int64_t)groups * f_tiles * m_tiles, sms / 2) * (p.k_blocks * (0.13 + 0.0007 * tile_f) + end) < best) {
     p.pair = true;
     p.spread = false;

@@ -10,7 +10,9 @@
 // token's consecutive features and stores them 32 bytes at a time (features as
 // M left a thread one 2-byte store per token and feature: 9000 cycles a tile,
 // twice the MMAs' time at K = 1024).  Rows that are not on 32 bytes are exchanged
-// within the warp first (4096 x 1000 x 2048: 25 us, value by value 52).  An element is the same sum of the same
+// within the warp first (4096 x 1000 x 2048: 22 us, value by value 52; 3000
+// tokens x 5000 fp32 and 15000 BF16 features x 232: 55, exchanged as single
+// features 91).  An element is the same sum of the same
 // products in the same order as with the operands exchanged.
 //
 // Roles: in both CTAs warp 0 copies its own tokens and its half of the features;
@@ -44,65 +46,112 @@ constexpr int kSetCols = kPairFeatures / 2;                     // accumulator c
 static_assert(kPairBSf + 8 * kSfRing <= 512, "TMEM");
 static_assert(kPairStages >= 4 && kPairStages <= 8, "stages");
 
+// Of N words a lane, word i of lane l of a group of N goes to word l of lane i.
+template <int N>
+__device__ __forceinline__ void exchange(uint32_t (&w)[N]) {
+#pragma unroll
+  for (int s = N / 2; s > 0; s >>= 1) {
+    const bool up = threadIdx.x & s;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(i & s)) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + s], s);
+        w[i] = up ? got : w[i];
+        w[i + s] = up ? w[i + s] : got;
+      }
+  }
+}
+
 // Stores of a warp's tokens (t0 + lane, below n_tok), features f, f + 1, ...,
 // f + n - 1 (of the weight), 16 at a time.  Where they lie in one segment, and
 // every token's on 32 bytes, a lane stores its token's 16 in one or two stores.
-// Else the 16 x 16 values of each half of the warp are exchanged, so that a
-// store is 16 neighbouring features of two tokens.
+// Else lanes exchange values first, so that a store is neighbouring features
+// of few tokens: in one segment pairs of features within 8 lanes (a store is 8
+// pairs of four tokens; two of single features where pairs are not aligned),
+// across segments single features within 16.
 struct TokenOut {
   const GemmOut* out;
   int t0, n_tok, f, n;
-  char* p;               // the lane's feature f, or null: no such token
-  bool bf16, wide;       // wide: 32-byte stores
+  char* row;             // token t0's feature f
+  int64_t step;          // bytes of a token's row
+  bool bf16, one, wide, even;   // one: one segment; wide, even: every token on 32 bytes, on a pair of values
 
   __device__ __forceinline__ TokenOut(const GemmOut& o, int t0_, int n_tok_, int f_, int n_)
-      : out(&o), t0(t0_), n_tok(n_tok_), f(f_), n(n_), p(nullptr), bf16(false), wide(false) {
+      : out(&o), t0(t0_), n_tok(n_tok_), f(f_), n(n_), row(nullptr), step(0), bf16(false), one(false), wide(false), even(false) {
     if (n <= 0) return;
     int sg = 0;
     while (sg + 1 < o.n_seg && f >= o.seg_end[sg]) ++sg;
-    const int r0 = sg > 0 ? o.seg_end[sg - 1] : 0;
-    bf16 = (o.bf16_mask >> sg) & 1u;
-    const int64_t t = t0 + (threadIdx.x & 31);
-    if (t < n_tok) p = static_cast<char*>(o.y[sg]) + (t * (o.seg_end[sg] - r0) + (f - r0)) * (bf16 ? 2 : 4);
-    wide = f + n <= o.seg_end[sg] && __all_sync(0xffffffffu, reinterpret_cast<uintptr_t>(p) % 32 == 0);
+    const int r0 = sg > 0 ? o.seg_end[sg - 1] : 0, el = (o.bf16_mask >> sg) & 1u ? 2 : 4;
+    bf16 = el == 2;
+    step = (int64_t)(o.seg_end[sg] - r0) * el;
+    row = static_cast<char*>(o.y[sg]) + t0 * step + (int64_t)(f - r0) * el;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row) | (n_tok - t0 > 1 ? step : 0);
+    one = f + n <= o.seg_end[sg];
+    wide = one && at % 32 == 0;
+    even = at % (2 * el) == 0;
   }
   __device__ __forceinline__ void put(int c, const uint32_t* v) const {       // features f + c .. f + c + 15
     if (c >= n) return;
-    if (wide && c + 16 <= n) {
-      if (p == nullptr) {
-      } else if (bf16) {
+    const int lane = threadIdx.x & 31;
+    if (one && c + 16 <= n) {
+      if (bf16) {
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
           w[e] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        tc::st_global_32b(p + 2 * c, w);
-      } else {
-        tc::st_global_32b(p + 4 * c, v);
-        tc::st_global_32b(p + 4 * c + 32, v + 8);
-      }
-      __syncwarp();
-      return;
-    }
-    const int lane = threadIdx.x & 31, fe = lane & 15;
-    float w[16];
+        if (wide) {
+          if (t0 + lane < n_tok) tc::st_global_32b(row + lane * step + 2 * c, w);
+        } else {
+          exchange(w);
+          char* q = row + (lane & 24) * step + 2 * c + 4 * (lane & 7);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(v[e]);
-#pragma unroll
-    for (int s = 8; s > 0; s >>= 1) {
-      const bool up = lane & s;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (!(i & s)) {
-          const float got = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + s], s);
-          w[i] = up ? got : w[i];
-          w[i + s] = up ? w[i + s] : got;
+          for (int i = 0; i < 8; ++i, q += step)
+            if (t0 + (lane & 24) + i < n_tok) {
+              if (even) {
+                *reinterpret_cast<uint32_t*>(q) = w[i];
+              } else {
+                reinterpret_cast<uint16_t*>(q)[0] = (uint16_t)w[i];
+                reinterpret_cast<uint16_t*>(q)[1] = (uint16_t)(w[i] >> 16);
+              }
+            }
         }
-    }
-    if (c + fe < n) {                                    // w[i]: this feature of token t0 + (lane & 16) + i
-      const int t = t0 + (lane & 16);
-      out_row(*out, f + c + fe).store16(t, n_tok - t, w);
+      } else if (wide) {
+        if (t0 + lane < n_tok) {
+          tc::st_global_32b(row + lane * step + 4 * c, v);
+          tc::st_global_32b(row + lane * step + 4 * c + 32, v + 8);
+        }
+      } else {
+        uint32_t a[8], b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) { a[e] = v[2 * e]; b[e] = v[2 * e + 1]; }
+        exchange(a);
+        exchange(b);
+        char* q = row + (lane & 24) * step + 4 * c + 8 * (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 8; ++i, q += step)
+          if (t0 + (lane & 24) + i < n_tok) {
+            if (even) {
+              *reinterpret_cast<uint2*>(q) = make_uint2(a[i], b[i]);
+            } else {
+              reinterpret_cast<uint32_t*>(q)[0] = a[i];
+              reinterpret_cast<uint32_t*>(q)[1] = b[i];
+            }
+          }
+      }
+    } else {
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e] = v[e];
+      exchange(w);
+      const int fe = lane & 15, t = t0 + (lane & 16);
+      if (c + fe < n) {                                  // w[i]: this feature of token t + i
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(w[e]);
+        out_row(*out, f + c + fe).store16(t, n_tok - t, x);
+      }
     }
     __syncwarp();
   }

@@ -295,6 +295,7 @@ FORMS = [
     (8001, 1032, 1, 450),         # pairs, output rows of odd length
     (6400, 10 * 528, 10, 780),    # pairs, grouped: feature tiles that begin inside a row tile
     (9456, 1160, 1, 513),         # pairs: two K parts, a ragged last tile, one token beyond two tiles
+    (8002, 1032, 1, 450),         # pairs, output rows on 4 and 8 bytes
 ]
 
 
@@ -325,7 +326,7 @@ def test_every_form_of_many_tokens(n_out, k_in, groups, n_tok):
 
 
 @pytest.mark.parametrize("n_out,k_in,n_tok", [(2368, 1536, 6), (2368, 1536, 50), (2368, 1536, 100), (700, 300 * 8, 300), (20001, 264, 300),
-                                              (9100, 1160, 513), (8001, 1032, 450), (9456, 1160, 513), (750, 8496, 639)])
+                                              (9100, 1160, 513), (8001, 1032, 450), (8002, 1032, 450), (9456, 1160, 513), (750, 8496, 639)])
 def test_segments_that_begin_anywhere(n_out, k_in, n_tok):
     """Segments of odd sizes, in every form of the launch: the outputs are
     those of one segment, and nothing beside them is written."""
