@@ -57,7 +57,7 @@ cudaError_t launch_gemm_bf16(const void* w_packed, int n_out, int k_in, int grou
                              const GemmOut& out, void* ws, int sms, cudaStream_t st);
 cudaError_t gemm_read_error(int32_t* code, int32_t* detail, cudaStream_t st);
 size_t fp8_weight_bytes(int n_out, int k_in, int groups);
-size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok);
+size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok, int sms);
 cudaError_t launch_fp8_pack_weight(const uint8_t* codes, const uint8_t* scales, int n_out, int k_in, int groups,
                                    uint8_t* w, cudaStream_t st);
 cudaError_t launch_fp8_quant_weight(const uint16_t* w, int n_out, int k_in, int groups, uint8_t* codes,
@@ -894,7 +894,8 @@ csa_status csa_gemm_fp8_pack_weight(const uint8_t* codes, const uint8_t* scales,
 size_t csa_gemm_fp8_workspace_bytes(int32_t n_out, int32_t k_in, int32_t groups, int32_t n_tok) {
   std::string why;
   if (!fp8_shape_ok(n_out, k_in, groups, &why) || n_tok < 1 || n_tok > CSA_FP8_MAX_TOKENS) return 0;
-  return csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok);
+  const int sms = sm_count();
+  return csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok, sms > 0 ? sms : 0);
 }
 
 csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32_t groups, const uint16_t* x,
@@ -915,7 +916,7 @@ csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32
     return fail(CSA_ERR_ARG, "w_packed must be 16-byte and workspace 256-byte aligned");
   const int sms = sm_count();
   if (sms <= 0) return fail(CSA_ERR_CUDA, "cannot query the SM count");
-  const size_t need = csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok);
+  const size_t need = csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok, sms);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(CSA_ERR_ARG, "workspace smaller than csa_gemm_fp8_workspace_bytes");
   cudaError_t e = csa::launch_gemm_fp8(w_packed, n_out, k_in, groups, x, n_tok, out, workspace, sms,

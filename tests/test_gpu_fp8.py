@@ -286,11 +286,18 @@ def test_refusals():
 
 # n_out, k_in, groups, n_tok
 FORMS = [
-    (257, 2056, 1, 130),          # a CTA per part: five token tiles of 32
+    (257, 10320, 1, 130),         # a CTA per part: five token tiles of 32
     (750, 8496, 1, 639),          # a CTA per part: five of 128
     (2051, 8200, 1, 130),         # a CTA per part: more clusters than the SMs hold at once
     (107, 2022 * 8, 1, 1030),     # one row tile, eight parts, 64 tokens a tile
-    (2022, 680, 1, 107),          # whole tiles of at most 128 tokens, four of 32
+    (2368, 1536, 1, 100),         # whole tiles of at most 128 tokens, four of 32
+    (2368, 7168, 1, 30),          # 32 tokens, a CTA per part
+    (20000, 264, 1, 30),          # 32 tokens, whole tiles, several per CTA
+    (2368, 7168, 1, 52),          # 64 tokens, a CTA per part
+    (9600, 1160, 1, 60),          # 64 tokens, whole tiles of two parts
+    (90, 264, 1, 1000),           # one launch: 63 tiles of 16 tokens
+    (512, 4096, 1, 70),           # one launch: five tiles, a cluster of eight CTAs each
+    (2048, 16 * 264, 16, 200),    # one launch: 13 tiles, grouped
     (8001, 264, 1, 1000),         # whole tiles, several per SM
     (8001, 1032, 1, 450),         # pairs, output rows of odd length
     (6400, 10 * 528, 10, 780),    # pairs, grouped: feature tiles that begin inside a row tile
@@ -300,22 +307,22 @@ FORMS = [
 
 
 @pytest.mark.parametrize("n_out,k_in,groups,n_tok", FORMS)
-def test_every_form_of_many_tokens(n_out, k_in, groups, n_tok):
+def test_every_form(n_out, k_in, groups, n_tok):
     """Against the oracle, in both types; the first tokens alone, which another
     form computes, have the same bits; rows behind the last stay as they were."""
     x, _, codes, scales = _inputs(n_out, k_in, groups, n_tok, n_tok)
     lin, xd = _linear(codes, scales, groups), x.cuda()
     y = torch.full((n_tok + 1, n_out), 7.0, device="cuda")
     lin(xd, y[:n_tok])
-    pick = np.unique(np.r_[0:8, n_tok // 2, n_tok - 40:n_tok])         # the oracle's share of the tokens
+    pick = np.unique(np.r_[0:8, n_tok // 2, n_tok - 20:n_tok])         # the oracle's share of the tokens
     _check(y[pick], x[pick], codes, scales, groups)
     b = torch.full((n_tok + 1, n_out), 7.0, device="cuda", dtype=torch.bfloat16)
     lin(xd, b[:n_tok])
     assert torch.equal(b[:n_tok], y[:n_tok].to(torch.bfloat16))
     assert bool((y[n_tok] == 7).all()) and bool((b[n_tok] == 7).all())
-    few = torch.empty((50, n_out), device="cuda")
-    lin(xd[:50], few)
-    assert torch.equal(few, y[:50])
+    few = torch.empty((25, n_out), device="cuda")
+    lin(xd[:25], few)
+    assert torch.equal(few, y[:25])
     need = lin.workspace_bytes(n_tok)                                  # the call stays within its workspace
     ws = torch.full((need + 4096,), 90, dtype=torch.uint8, device="cuda")
     b.zero_()
