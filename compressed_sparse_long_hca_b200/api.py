@@ -792,12 +792,27 @@ def quantize_fp8_weight(w, device: str | torch.device = "cuda", stream=None):
     exponents [ceil(n_out / 128), ceil(k / 128)]) of a real weight [n_out, k]
     (host array or tensor; rounded to BF16 first; or a host array of BF16 bit
     patterns as uint16), through csa_gemm_fp8_quant_weight.  A block with an infinity or a NaN gets the
-    NaN scale (255)."""
+    NaN scale (255).  With `stream` everything, the conversion to BF16 and the
+    allocations too, belongs to that stream, which first waits for the work
+    queued on the current one (w may come from there); a reader of the codes
+    and scales on another stream waits for it."""
     if not isinstance(w, torch.Tensor):
         w = np.ascontiguousarray(w)
         w = torch.from_numpy(w).view(torch.bfloat16) if w.dtype == np.uint16 else torch.from_numpy(w.astype(np.float32))
     if w.dim() != 2 or not w.is_floating_point():
         raise ValueError("w must be a real matrix [n_out, k]")
+    if stream is None:
+        return _quantize_fp8(w, device, None)
+    stream.wait_stream(torch.cuda.current_stream(stream.device))
+    with torch.cuda.stream(stream):
+        out = _quantize_fp8(w, device, stream)
+    if w.is_cuda:
+        w.record_stream(stream)                          # the caller may drop w before the stream has read it
+    return out
+
+
+def _quantize_fp8(w: torch.Tensor, device, stream):
+    """quantize_fp8_weight's work, with `stream` (if any) the current one."""
     if not w.is_cuda:
         w = w.to(device)
     w = w.to(torch.bfloat16).contiguous()
