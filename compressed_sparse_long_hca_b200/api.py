@@ -41,6 +41,14 @@ def _need(t, dtype, shape=None, name="tensor"):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _aligned(workspace: torch.Tensor) -> tuple[int, int]:
+    """The first address of a workspace on 256 bytes, and the bytes from there
+    to its end (0 for a workspace that ends before)."""
+    base = workspace.data_ptr()
+    at = (base + 255) // 256 * 256
+    return at, max(0, workspace.numel() - (at - base))
+
+
 class Cache:
     """A CSA/HCA cache living in one caller-owned device buffer (the arena).
 
@@ -153,8 +161,7 @@ class Cache:
                     self._tk_ws = ws
                 workspace = ws
             _need(workspace, torch.uint8, name="workspace")
-            ws_ptr = (workspace.data_ptr() + 255) // 256 * 256
-            ws_bytes = workspace.numel() - (ws_ptr - workspace.data_ptr())
+            ws_ptr, ws_bytes = _aligned(workspace)
         check(self.lib.csa_index_topk(self.handle, layer, n, _ptr(req_ids), _ptr(q_idx), _ptr(w), _ptr(scores),
                                       scores.shape[1], _ptr(n_valid), k, _ptr(idx_out), ws_ptr, ws_bytes,
                                       VARIANTS[variant], _stream(stream)), "csa_index_topk")
@@ -253,8 +260,7 @@ class Cache:
                 self._pf_ws = ws
             workspace = ws
         _need(workspace, torch.uint8, name="workspace")
-        ws_ptr = (workspace.data_ptr() + 255) // 256 * 256
-        ws_bytes = workspace.numel() - (ws_ptr - workspace.data_ptr())
+        ws_ptr, ws_bytes = _aligned(workspace)
         check(self.lib.csa_prefill_chunk(self.handle, layer, n, _ptr(req_ids), n_tok, _ptr(kv_cand), _ptr(kv_gate),
                                          _ptr(idx_cand), _ptr(idx_gate), _ptr(q), _ptr(q_idx), _ptr(w), k,
                                          _ptr(sink), scale, _ptr(out), _ptr(topk_out), ws_ptr, ws_bytes,
@@ -642,8 +648,7 @@ class Linear:
             if self._ws is None or self._ws.numel() < need + 256 or self._ws.device != x.device:
                 self._ws = torch.empty(need + 256, dtype=torch.uint8, device=x.device)
             workspace = self._ws
-        ws_ptr = (workspace.data_ptr() + 255) // 256 * 256
-        ws_bytes = workspace.numel() - (ws_ptr - workspace.data_ptr())
+        ws_ptr, ws_bytes = _aligned(workspace)
         check(self.lib.csa_gemm_bf16(self.packed.data_ptr(), self.n_out, self.k_in, self.groups, _ptr(x), n,
                                      len(segs), arr, ws_ptr, ws_bytes, _stream(stream)), "csa_gemm_bf16")
 
@@ -773,9 +778,7 @@ class LinearFP8:
             if workspace.device != self.device:
                 raise ValueError("workspace must be on the weight's device")
         if workspace is not None:
-            base = workspace.data_ptr()
-            at = (base + 255) // 256 * 256
-            size = workspace.numel() - (at - base)
+            at, size = _aligned(workspace)
         status = _on_device(index, self.lib.csa_gemm_fp8, self.packed.data_ptr(), self.n_out, self.k_in, self.groups,
                             x.data_ptr(), n, n_seg, segs, at, size, _raw_stream(stream, index))
         if status:

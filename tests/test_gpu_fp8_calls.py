@@ -50,3 +50,16 @@ def test_a_weight_quantised_on_another_stream():
                 lin(x, y)
                 assert torch.equal(y, want)
     LinearFP8.check_device_error()
+
+
+def test_a_short_workspace_off_its_alignment_is_refused():
+    from compressed_sparse_long_hca_b200.api import Linear, LinearFP8
+    w = np.zeros((2368, 1536), np.float32)
+    x, y = torch.zeros((100, 1536), dtype=torch.bfloat16, device="cuda"), torch.full((100, 2368), 5.0, device="cuda")
+    ws = torch.zeros(1024, dtype=torch.uint8, device="cuda")
+    assert ws.data_ptr() % 256 == 0
+    for lin in (LinearFP8.quantize(w), Linear(w)):
+        with pytest.raises(RuntimeError, match="workspace"):
+            lin(x, y, workspace=ws[1:101])
+    torch.cuda.synchronize()
+    assert bool((y == 5).all())

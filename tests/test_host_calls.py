@@ -95,3 +95,52 @@ def test_a_weight_is_quantised_on_one_stream(streams, where):
         if stream is not None:
             assert stream.waited == ["current"]
             assert (id(w), "side") in streams.recorded or where != "device tensor"
+
+
+def _short_view():
+    """100 bytes that end before the next 256-byte boundary."""
+    buf = torch.zeros(1024, dtype=torch.uint8)
+    skip = -buf.data_ptr() % 256 + 1
+    return buf[skip: skip + 100]
+
+
+class Sizes:
+    """A library that needs 512 bytes of scratch and notes the size it is given (the argument at `place`)."""
+
+    def __init__(self, **place):
+        self.place, self.got = place, None
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return lambda *args: 512
+
+        def call(*args):
+            self.got = ctypes.c_size_t(args[self.place[name]]).value
+            return 0
+        return call
+
+
+@pytest.mark.parametrize("entry", ["index_topk", "prefill_chunk", "Linear", "LinearFP8"])
+def test_a_workspace_shorter_than_its_alignment_counts_nothing(monkeypatch, entry):
+    """The library then refuses the call: no size wraps around."""
+    monkeypatch.setattr(api, "_need", lambda *args, **kw: None)
+    monkeypatch.setattr(api, "_stream", lambda stream: None)
+    monkeypatch.setattr(api, "_raw_stream", lambda stream, index: None)
+    monkeypatch.setattr(api, "_on_device", lambda index, call, *args: call(*args))
+    ws, f = _short_view(), torch.float32
+    lib = Sizes(csa_index_topk=12, csa_prefill_chunk=18, csa_gemm_bf16=9, csa_gemm_fp8=9)
+    if entry in ("index_topk", "prefill_chunk"):
+        c = object.__new__(api.Cache)
+        c.handle, c.lib, c.n_csa, c.H, c.D, c.H_I, c.d_I, c.qdtype = None, lib, 1, 1, 8, 1, 32, torch.bfloat16
+        ids, t = torch.zeros(1, dtype=torch.int32), torch.zeros
+        if entry == "index_topk":
+            c.index_topk(0, ids, t(1, 1, 32), t(1, 1), t(1, 128), ids, 4, ids, workspace=ws)
+        else:
+            c.prefill_chunk(0, ids, t(1, 2, 8), t(1, 2, 8), t(1, 2, 32), t(1, 2, 32), t(1, 2, 1, 8), t(1, 2, 1, 32), t(1, 2, 1), 4,
+                            t(1), t(1, 2, 1, 8), workspace=ws)
+    else:
+        lin = object.__new__(getattr(api, entry))
+        lin.lib, lin.n_out, lin.k_in, lin.groups, lin.device, lin._index, lin._need_bytes = lib, 4, 8, 1, ws.device, -1, {}
+        lin.packed = torch.zeros(8, dtype=torch.uint8)
+        lin(torch.zeros((20, 8), dtype=torch.bfloat16), torch.zeros((20, 4), dtype=f), workspace=ws)
+    assert lib.got == 0
