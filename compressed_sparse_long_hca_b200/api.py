@@ -804,8 +804,13 @@ def quantize_fp8_weight(w, device: str | torch.device = "cuda", stream=None):
         w = torch.from_numpy(w).view(torch.bfloat16) if w.dtype == np.uint16 else torch.from_numpy(w.astype(np.float32))
     if w.dim() != 2 or not w.is_floating_point():
         raise ValueError("w must be a real matrix [n_out, k]")
+    on = w.device if w.is_cuda else torch.device(device)
+    if on.type != "cuda":
+        raise ValueError("device must be a CUDA device")
     if stream is None:
         return _quantize_fp8(w, device, None)
+    if on.index not in (None, stream.device.index):
+        raise ValueError("stream must be on the weight's device")
     stream.wait_stream(torch.cuda.current_stream(stream.device))
     with torch.cuda.stream(stream):
         out = _quantize_fp8(w, device, stream)

@@ -46,13 +46,17 @@ class Streams(TorchFunctionMode):
         name = getattr(func, "__name__", "")
         if func == torch.Tensor.is_cuda.__get__:
             return id(args[0]) in self.cuda
+        if func == torch.Tensor.device.__get__ and id(args[0]) in self.cuda:
+            return torch.device("cuda", 0)
         there = any(id(a) in self.cuda for a in args)
+        if name == "empty":
+            there, kwargs = str(kwargs["device"]).startswith("cuda"), {**kwargs, "device": "cpu"}
         if name == "to" and str(args[1]).startswith("cuda"):
             args, there = (args[0], "cpu"), True
             out = args[0].clone()
         else:
             out = func(*args, **kwargs)
-        if name in ("to", "contiguous", "empty") and (there or name == "empty"):
+        if name in ("to", "contiguous", "empty") and there:
             self.work.append((name, self.current.name))
         return self.on_cuda(out) if isinstance(out, torch.Tensor) and there else out
 
@@ -95,6 +99,19 @@ def test_a_weight_is_quantised_on_one_stream(streams, where):
         if stream is not None:
             assert stream.waited == ["current"]
             assert (id(w), "side") in streams.recorded or where != "device tensor"
+
+
+@pytest.mark.parametrize("stream", [None, FakeStream("side")])
+def test_a_weight_is_quantised_on_a_cuda_device_alone(streams, stream):
+    """Nothing is launched for host memory, nor on another device's stream."""
+    a = np.ones((8, 16), np.float32)
+    with streams:
+        with pytest.raises(ValueError, match="device"):
+            api.quantize_fp8_weight(a, device="cpu", stream=stream)
+        if stream is not None:
+            with pytest.raises(ValueError, match="device"):
+                api.quantize_fp8_weight(a, device="cuda:1", stream=stream)
+    assert not streams.work
 
 
 def _short_view():
