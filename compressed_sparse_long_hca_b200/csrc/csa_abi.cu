@@ -949,6 +949,8 @@ csa_status csa_head_norm(int64_t n_tok, int32_t dim, int32_t rope, double eps, c
       return fail(CSA_ERR_ARG, "x, y or weight is not aligned to its elements");
     const bool rotate = p->rotate && rope > 0;
     if (rotate && (!positions || !theta)) return fail(CSA_ERR_ARG, "rotated heads need positions and theta");
+    if (rotate && (reinterpret_cast<uintptr_t>(positions) % 8 || reinterpret_cast<uintptr_t>(theta) % 8))
+      return fail(CSA_ERR_ARG, "positions and theta must be 8-byte aligned");
     a.part[s] = csa::HeadNormPart{p->x, p->y, p->weight, p->x_token_stride, p->x_head_stride, p->y_token_stride,
                                   p->y_head_stride, p->heads, p->f32 ? 1 : 0, rotate ? 1 : 0, 0, 0, 0, 0};
     heads += p->heads;

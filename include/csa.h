@@ -614,8 +614,8 @@ csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32
  *   n_tok      0 .. 2^31 - 1 (heads x tokens so that the launch has at most
  *              2^31 - 1 blocks; a block takes at least 4 heads)
  *   dim        even, 2 .. 1024;  rope even, 0 .. dim;  eps in [0, 1e30]
- *   positions  device int64 [n_tok], theta device fp64 [rope / 2]; may be
- *              NULL when nothing is rotated
+ *   positions  device int64 [n_tok], theta device fp64 [rope / 2], 8-byte
+ *              aligned; may be NULL when nothing is rotated
  *   q, k       host descriptors, read during the call; NULL or heads = 0:
  *              none.  x and y: device, element (token t, head h, dim d) at
  *              t * token_stride + h * head_stride + d (strides in elements;

@@ -245,3 +245,18 @@ def test_an_fp8_workspace_serves_every_smaller_call(cuda_lib):
         assert sizes[:16] == [0] * 16
         assert all(a <= b for a, b in zip(sizes, sizes[1:]))
         assert all(s >= n * k_in for n, s in enumerate(sizes, 1) if s)
+
+
+def _head_part(**kw):
+    P = 0x10000
+    d = dict(x=P, y=P, weight=P, x_token_stride=512, x_head_stride=64, y_token_stride=512, y_head_stride=64, heads=8,
+             f32=1, rotate=1)
+    d.update(kw)
+    return ctypes.cast(ctypes.pointer(_lib.HeadNormPart(*[d[n] for n, _ in _lib.HeadNormPart._fields_])), ctypes.c_void_p)
+
+
+def test_head_norm_refuses_positions_and_angles_off_their_elements(cuda_lib):
+    P = 0x10000
+    for pos, theta in ((P + 4, P), (P, P + 4), (P + 1, P)):
+        assert cuda_lib.csa_head_norm(4, 64, 16, 1e-6, pos, theta, _head_part(), None, None) == -1, (pos, theta)
+        assert b"8-byte aligned" in cuda_lib.csa_last_error()
