@@ -899,7 +899,8 @@ class HeadNorm:
         type and number of heads); any token and head strides, dims
         contiguous.  q_out, k_out: outputs of the same type and shape (other
         strides are fine), None for in place; an output is its input or does
-        not overlap any.  positions: CUDA int64 [n], the tokens' positions
+        not overlap any, and its heads do not overlap each other (an expanded
+        tensor is an input only).  positions: CUDA int64 [n], the tokens' positions
         (None when nothing is rotated).  Returns (q_out, k_out)."""
         n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else -1
         q_out = q if q_out is None else q_out

@@ -925,6 +925,26 @@ csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32
   return CSA_OK;
 }
 
+// Whether two heads of an output share memory: token t's head h takes `dim`
+// elements from t * tok + h * head on.
+static bool heads_overlap(int64_t n_tok, int64_t tok, int64_t heads, int64_t head, int64_t dim) {
+  __int128 a = tok < 0 ? -(__int128)tok : tok, b = head < 0 ? -(__int128)head : head;     // (the sign moves nothing together)
+  int64_t na = n_tok, nb = heads;
+  if ((na > 1 && a < dim) || (nb > 1 && b < dim)) return true;
+  if (na == 1 || nb == 1) return false;
+  if (a < b) { std::swap(a, b); std::swap(na, nb); }
+  if (a >= b * (nb - 1) + dim) return false;             // one dimension's run lies within a step of the other
+  if (nb > na) {                                         // the fewer steps of the two are gone through
+    std::swap(a, b);
+    std::swap(na, nb);
+  }
+  for (int64_t i = 1; i < nb; ++i) {                     // i steps of b against the nearest steps of a
+    const __int128 j = i * b / a;
+    if ((j < na && i * b - j * a < dim) || (j + 1 < na && (j + 1) * a - i * b < dim)) return true;
+  }
+  return false;
+}
+
 csa_status csa_head_norm(int64_t n_tok, int32_t dim, int32_t rope, double eps, const int64_t* positions,
                          const double* theta, const csa_head_norm_part* q, const csa_head_norm_part* k,
                          csa_stream_t stream) {
@@ -947,6 +967,8 @@ csa_status csa_head_norm(int64_t n_tok, int32_t dim, int32_t rope, double eps, c
     if (reinterpret_cast<uintptr_t>(p->x) % el || reinterpret_cast<uintptr_t>(p->y) % el ||
         reinterpret_cast<uintptr_t>(p->weight) % 4)
       return fail(CSA_ERR_ARG, "x, y or weight is not aligned to its elements");
+    if (heads_overlap(n_tok, p->y_token_stride, p->heads, p->y_head_stride, dim))
+      return fail(CSA_ERR_ARG, "heads of an output overlap each other");
     const bool rotate = p->rotate && rope > 0;
     if (rotate && (!positions || !theta)) return fail(CSA_ERR_ARG, "rotated heads need positions and theta");
     if (rotate && (reinterpret_cast<uintptr_t>(positions) % 8 || reinterpret_cast<uintptr_t>(theta) % 8))

@@ -622,7 +622,9 @@ csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32
  *              dims contiguous), fp32 when `f32`, else BF16, aligned to
  *              their elements (on 16 bytes with dim a multiple of 8 the
  *              loads are 16 bytes wide).  y may be x with its strides (in
- *              place); otherwise no output may overlap an input.  weight:
+ *              place); otherwise no output may overlap an input.  Heads of
+ *              x may lie on each other (a stride of 0), those of y may not
+ *              (CSA_ERR_ARG), in place either.  weight:
  *              device fp32 [dim], or NULL for ones.  rotate: whether the
  *              last dims are rotated.
  * Asynchronous.

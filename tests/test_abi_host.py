@@ -260,3 +260,20 @@ def test_head_norm_refuses_positions_and_angles_off_their_elements(cuda_lib):
     for pos, theta in ((P + 4, P), (P, P + 4), (P + 1, P)):
         assert cuda_lib.csa_head_norm(4, 64, 16, 1e-6, pos, theta, _head_part(), None, None) == -1, (pos, theta)
         assert b"8-byte aligned" in cuda_lib.csa_last_error()
+
+
+def test_head_norm_refuses_an_output_whose_heads_overlap(cuda_lib):
+    """Against every pair of heads, for strides of either sign and order."""
+    import itertools
+    P, dim = 0x10000, 4
+    for n, heads in ((1, 1), (1, 3), (3, 1), (2, 3), (3, 2), (4, 5)):
+        for ts, hs in itertools.product((-14, -8, -3, 0, 1, 4, 6, 8, 9, 12, 20), (-12, -4, 0, 2, 4, 5, 8, 10, 16)):
+            at = [t * ts + h * hs for t in range(n) for h in range(heads)]
+            overlap = any(abs(a - b) < dim for a, b in itertools.combinations(at, 2))
+            part = _head_part(heads=heads, y_token_stride=ts, y_head_stride=hs, rotate=0)
+            # (the keys are refused in any case, so that nothing is launched)
+            assert cuda_lib.csa_head_norm(n, dim, 0, 1e-6, None, None, part, _head_part(heads=-1), None) == -1
+            assert (b"overlap" in cuda_lib.csa_last_error()) == overlap, (n, heads, ts, hs)
+    wide = _head_part(heads=65536, y_token_stride=1 << 62, y_head_stride=-(1 << 62), rotate=0)
+    assert cuda_lib.csa_head_norm((1 << 31) - 1, 1024, 0, 1e-6, None, None, wide, _head_part(heads=-1), None) == -1
+    assert b"overlap" in cuda_lib.csa_last_error()
