@@ -857,6 +857,7 @@ csa_status csa_gemm_bf16(const void* w_packed, int32_t n_out, int32_t k_in, int3
 static bool fp8_shape_ok(int32_t n_out, int32_t k_in, int32_t groups, std::string* why) {
   if (!gemm_shape_ok(n_out, k_in, groups, why)) return false;
   if (n_out > 65535 * 128) { *why = "n_out must be <= 65535 * 128"; return false; }
+  if (k_in / groups > 0x7FFFFFFF - 127) { *why = "k_in / groups must be <= 2^31 - 128"; return false; }
   return true;
 }
 

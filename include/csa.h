@@ -563,7 +563,8 @@ csa_status csa_gemm_check_device_error(csa_stream_t stream);
  *   csa_gemm_fp8_weight_bytes   device bytes of a packed weight (0 for a bad
  *                           shape: groups must divide n_out and k_in, with
  *                           groups > 1 n_out / groups is a multiple of 128,
- *                           k_in / groups is a multiple of 8)
+ *                           k_in / groups is a multiple of 8 and at most
+ *                           2^31 - 128, n_out at most 65535 * 128)
  *   csa_gemm_fp8_quant_weight   device BF16 W -> device codes and scales;
  *                           asynchronous
  *   csa_gemm_fp8_pack_weight    device codes and scales -> packed tiles

@@ -277,3 +277,14 @@ def test_head_norm_refuses_an_output_whose_heads_overlap(cuda_lib):
     wide = _head_part(heads=65536, y_token_stride=1 << 62, y_head_stride=-(1 << 62), rotate=0)
     assert cuda_lib.csa_head_norm((1 << 31) - 1, 1024, 0, 1e-6, None, None, wide, _head_part(heads=-1), None) == -1
     assert b"overlap" in cuda_lib.csa_last_error()
+
+
+def test_fp8_gemm_refuses_rows_whose_blocks_cannot_be_counted(cuda_lib):
+    P, most = 0x10000, (1 << 31) - 128
+    wb = cuda_lib.csa_gemm_fp8_weight_bytes
+    assert wb(1, most, 1) == (most // 128) * 16384 + -(-most // 512) * (512 + 1024)
+    for k in (most + 8, most + 120):
+        assert wb(1, k, 1) == 0
+        assert cuda_lib.csa_gemm_fp8_workspace_bytes(1, k, 1, 100) == 0
+        assert cuda_lib.csa_gemm_fp8_quant_weight(P, 1, k, 1, P, P, None) == -1
+        assert cuda_lib.csa_gemm_fp8_pack_weight(P, P, 1, k, 1, P, 1 << 60, None) == -1
