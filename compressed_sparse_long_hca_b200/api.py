@@ -684,6 +684,22 @@ def _scratch(nbytes: int, device: torch.device, stream) -> torch.Tensor:
 _GEMM_OUT = struct.Struct("@iiP")                    # csa_gemm_out
 
 
+class _DeviceCheck:
+    """check_device_error(stream=None) of a class whose objects each have a
+    device (the library's error words are per device): an object's own, the
+    class's the stream's device or else the current one."""
+
+    def __get__(self, obj, owner=None):
+        def check_device_error(stream=None) -> None:
+            """Raises the first device error since the last check (waits for `stream`)."""
+            if obj is not None:
+                index = obj._index
+            else:
+                index = torch.cuda.current_device() if stream is None else stream.device.index
+            check(_on_device(index, _lib.load().csa_gemm_check_device_error, _raw_stream(stream, index)), "gemm device")
+        return check_device_error
+
+
 class LinearFP8:
     """A weight in 8-bit floating point with one power-of-two scale per
     128 x 128 block, packed once for csa_gemm_fp8: Y[t][o] = sum_k X[t][k]
@@ -785,9 +801,7 @@ class LinearFP8:
             check(status, "csa_gemm_fp8")
         return outs
 
-    @staticmethod
-    def check_device_error(stream=None) -> None:
-        check(_lib.load().csa_gemm_check_device_error(_stream(stream)), "gemm device")
+    check_device_error = _DeviceCheck()
 
 
 def quantize_fp8_weight(w, device: str | torch.device = "cuda", stream=None):

@@ -519,8 +519,9 @@ csa_status csa_prefill_chunk(csa_cache_t* cache, int32_t layer, int32_t n, const
  *                           256-byte aligned, owned by the caller, not used
  *                           by other work until the call's kernels finish.
  *                           Asynchronous on `stream`.
- *   csa_gemm_check_device_error  read and clear the GEMM's device error word
- *                           (a bounded pipeline wait that gave up);
+ *   csa_gemm_check_device_error  read and clear the GEMM's error word on the
+ *                           current device (a bounded pipeline wait that
+ *                           gave up);
  *                           synchronises `stream`.
  * ------------------------------------------------------------------- */
 typedef struct {

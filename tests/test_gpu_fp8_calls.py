@@ -63,3 +63,6 @@ def test_a_short_workspace_off_its_alignment_is_refused():
             lin(x, y, workspace=ws[1:101])
     torch.cuda.synchronize()
     assert bool((y == 5).all())
+    lin = LinearFP8.quantize(w)
+    lin.check_device_error()
+    lin.check_device_error(torch.cuda.Stream())

@@ -161,3 +161,25 @@ def test_a_workspace_shorter_than_its_alignment_counts_nothing(monkeypatch, entr
         lin.packed = torch.zeros(8, dtype=torch.uint8)
         lin(torch.zeros((20, 8), dtype=torch.bfloat16), torch.zeros((20, 4), dtype=f), workspace=ws)
     assert lib.got == 0
+
+
+def test_device_errors_are_read_where_the_weight_is(monkeypatch):
+    asked = []
+
+    class Lib:
+        @staticmethod
+        def csa_gemm_check_device_error(stream):
+            return 0
+
+    monkeypatch.setattr(api._lib, "load", lambda: Lib)
+    monkeypatch.setattr(api, "_on_device", lambda index, call, *args: asked.append((index, *args)) or call(*args))
+    monkeypatch.setattr(api, "_raw_stream", lambda stream, index: ("current", index) if stream is None else stream.cuda_stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(api, "_stream", lambda stream: ("current", 0) if stream is None else stream.cuda_stream)
+    lin, side = object.__new__(api.LinearFP8), FakeStream("side")
+    lin._index, side.device = 3, torch.device("cuda", 2)
+    lin.check_device_error()
+    lin.check_device_error(side)
+    api.LinearFP8.check_device_error()
+    api.LinearFP8.check_device_error(side)
+    assert asked == [(3, ("current", 3)), (3, 16), (0, ("current", 0)), (2, 16)]
