@@ -916,9 +916,14 @@ class HeadNorm:
         not overlap any, and its heads do not overlap each other (an expanded
         tensor is an input only).  positions: CUDA int64 [n], the tokens' positions
         (None when nothing is rotated).  Returns (q_out, k_out)."""
-        n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else -1
         q_out = q if q_out is None else q_out
         k_out = k if k_out is None else k_out
+        self._launch(self._checked(positions, q, q_out, k, k_out), stream)
+        return q_out, k_out
+
+    def _checked(self, positions, q, q_out, k, k_out) -> tuple:
+        """The checks of a call, and what its launch takes."""
+        n = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else -1
         part = self._part(q, q_out, self._q_weight, self.rope > 0, n, "q")
         k_part = None if k is None else self._part(k, k_out, self._k_weight, self.rotate_k, n, "k")
         pos = None
@@ -927,11 +932,14 @@ class HeadNorm:
                     or positions.shape[0] != n or positions.get_device() != self._index or not positions.is_contiguous():
                 raise ValueError(f"positions must be contiguous int64 [{n}] on {self.device}")
             pos = positions.data_ptr()
+        return n, pos, part, k_part
+
+    def _launch(self, checked: tuple, stream) -> None:
+        n, pos, part, k_part = checked
         status = _on_device(self._index, self.lib.csa_head_norm, n, self.dim, self.rope, self.eps, pos, self._theta, part,
                             k_part, _raw_stream(stream, self._index))
         if status:
             check(status, "csa_head_norm")
-        return q_out, k_out
 
 
 _HEAD_NORM_PART = struct.Struct("@PPPqqqqiii4x")     # csa_head_norm_part
@@ -999,8 +1007,10 @@ class LayerProjections:
 
     def __call__(self, h: torch.Tensor, outs: dict, stream=None, positions: torch.Tensor | None = None) -> dict:
         """positions: CUDA int64 [n], the tokens' positions (with a norm that
-        rotates)."""
+        rotates; without them nothing is launched)."""
         n = h.shape[0]
+        # (what the norm would refuse is refused before the products are launched)
+        checked = None if self.norm is None else self.norm._checked(positions, outs["q"], outs["q"], outs["c"], outs["c"])
         seg1 = [outs["c"].view(n, -1), outs["z"].view(n, -1)]
         if self.csa:
             seg1 += [outs["ci"].view(n, -1), outs["zi"].view(n, -1), outs["w"]]
@@ -1008,8 +1018,8 @@ class LayerProjections:
         self.W1(h, seg1, stream=stream)
         seg2 = [outs["q"].view(n, -1)] + ([outs["q_idx"].view(n, -1)] if self.csa else [])
         self.W2(outs["c_q"], seg2, stream=stream)
-        if self.norm is not None:
-            self.norm(positions, outs["q"], None, outs["c"], None, stream=stream)
+        if checked is not None:
+            self.norm._launch(checked, stream)
         return outs
 
 

@@ -183,3 +183,24 @@ def test_device_errors_are_read_where_the_weight_is(monkeypatch):
     api.LinearFP8.check_device_error()
     api.LinearFP8.check_device_error(side)
     assert asked == [(3, ("current", 3)), (3, 16), (0, ("current", 0)), (2, 16)]
+
+
+def test_projections_with_a_norm_refuse_bad_positions_before_the_first_launch():
+    """The products would overwrite the outputs, which stay without their norm."""
+    n, d, D, H, d_c = 3, 16, 8, 2, 16
+    norm = object.__new__(api.HeadNorm)
+    norm.dim, norm.rope, norm.rotate_k, norm._index, norm.device = D, 4, False, -1, torch.device("cpu")
+    norm._q_weight = norm._k_weight = 0
+    launched = []
+    P = object.__new__(api.LayerProjections)
+    P.csa, P.norm = False, norm
+    P.W1 = P.W2 = lambda *args, **kw: launched.append(args)
+    outs = dict(c=torch.zeros(n, 1, D), z=torch.zeros(n, 1, D), c_q=torch.zeros(n, d_c, dtype=torch.bfloat16),
+                q=torch.zeros(n, H, D, dtype=torch.bfloat16))
+    h = torch.zeros(n, d, dtype=torch.bfloat16)
+    for bad in (None, torch.zeros(n), torch.zeros(n + 1, dtype=torch.int64), torch.zeros((n, 1), dtype=torch.int64)):
+        with pytest.raises(ValueError, match="positions"):
+            P(h, outs, positions=bad)
+    with pytest.raises(ValueError, match="q must be"):
+        P(h, {**outs, "q": outs["q"][:, :, :4]}, positions=torch.zeros(n, dtype=torch.int64))
+    assert not launched
