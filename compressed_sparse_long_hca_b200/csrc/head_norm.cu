@@ -379,12 +379,16 @@ __global__ void __launch_bounds__(kHnThreads, kPerSm) head_norm_kernel(const __g
   if (has_k) norm_part<NC, false>(a, k, t, 1, kb * k.block_heads, min(k.heads, (kb + 1) * k.block_heads), cs, table && !has_q);
 }
 
+// Blocks an SM holds of the kernel below for NC steps (168 registers a thread
+// with NC = 4, at most 128 else).
+constexpr int run_per_sm(int nc) { return nc > 2 ? 3 : 4; }
+
 // A block works on a run of tokens.  The heads of all tokens, a token's queries
 // before its keys, are one list in which a head costs its values' bytes; a
 // block takes `share` of the list's cost.  The tokens whose sines fit are done
 // at a time, their queries and then their keys.
 template <int NC>
-__global__ void __launch_bounds__(kHnThreads, NC == 4 ? 3 : 4) head_norm_run_kernel(const __grid_constant__ HeadNormArgs a) {
+__global__ void __launch_bounds__(kHnThreads, run_per_sm(NC)) head_norm_run_kernel(const __grid_constant__ HeadNormArgs a) {
   __shared__ float2 cs[kHnMaxDim / 2];
   tc::griddep_launch_dependents();
   tc::griddep_wait();
@@ -448,7 +452,7 @@ cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st) {
   // heads of 256, 10 passes: 18 instead of 23; but 2048 x 72 heads of 128, 9
   // passes: BF16 29 instead of 25, fp32 49 instead of 41; and in less than two
   // waves, 500 x 3 of 64: 4.8 instead of 4.2.)
-  const int64_t wave = (nc == 4 ? 3LL : 4LL) * sms;
+  const int64_t wave = (int64_t)run_per_sm(nc) * sms;
   const bool many = grid > 2 * wave;
   const int passes = (a.part[0].heads + a.part[1].heads + slots - 1) / slots;
   const bool run = many && passes <= (nc == 2 && !a.part[a.part[0].heads ? 0 : 1].f32 ? 10 : 6);
