@@ -60,7 +60,7 @@ struct Fp8Args {
   const uint8_t* w;       // packed weight: tiles [row_tiles][k_blocks][16 KB]
   const uint8_t* wsf;     // its scales: chunks [row_tiles][sup][512]
   const uint8_t* xp;      // packed activations [groups][k_blocks][tok_tiles][tile_n * 128]
-  const uint8_t* xsf;     // their scales: chunks [groups][sup][tok_tiles][chunks][512]
+  const uint8_t* xsf;     // their scales: chunks [groups][sup][tok_tiles][512]
   const uint16_t* x;      // fused quantisation: the BF16 tokens [n_tok][groups * kg]
   int x_aligned;          // x on 16 bytes (every block's row then is: kg is a multiple of 8)
   int kg;
@@ -86,7 +86,6 @@ struct Cfg {
   static constexpr int kThreads = 64 + kEpi + (FUSE ? 256 : 0);
   static constexpr int kAccs = ONE ? 1 : 2;
   static constexpr int kPerSm = NT <= 64 || ONE ? 2 : 1;   // CTAs per SM
-  static constexpr int kChunks = (NT + 127) / 128;         // scale chunks of a token tile
   // Fused: the tokens' blocks have slots of their own beside the ring, filled
   // a batch at a time (the loads of a batch, 32 registers a thread, are in
   // flight at once) by four warps, so that the quantiser works ahead of the
@@ -95,15 +94,16 @@ struct Cfg {
   static constexpr int kBatch = 4, kBatches = 2;
   static constexpr int kSlotBytes = NT * kKBlk + kSfBytes;
   static constexpr int kSlots = FUSE ? kBatch * kBatches * kSlotBytes : 0;
-  static constexpr int kStageBytes = kWTileBytes + kSfBytes + (FUSE ? 0 : NT * kKBlk + kSfBytes * kChunks);
+  static constexpr int kStageBytes = kWTileBytes + kSfBytes + (FUSE ? 0 : NT * kKBlk + kSfBytes);
   static constexpr int kStagesFit = ((kPerSm == 2 ? 110 : 224) * 1024 - kSlots) / kStageBytes;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
   // TMEM: the accumulators, the weight's scale ring, the tokens' scale ring
   static constexpr uint32_t kXsfRing = FUSE ? 8 : kSfRing;
   static constexpr uint32_t kWsfBase = kAccs * NT, kXsfBase = kWsfBase + 4 * kSfRing;
-  static constexpr uint32_t kColsNeeded = kXsfBase + 4 * kChunks * kXsfRing;
+  static constexpr uint32_t kColsNeeded = kXsfBase + 4 * kXsfRing;
   static constexpr uint32_t kTmemCols = kColsNeeded <= 128 ? 128 : kColsNeeded <= 256 ? 256 : 512;
   static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kSlots + 256 + 128;   // ring, barriers, alignment
+  static_assert(NT <= 128, "a token tile's scales are one chunk");
   static_assert(kColsNeeded <= 512 && kTmemCols * kPerSm <= 512, "TMEM");
   static_assert(kStages >= 3 && kStages <= 8, "stages");
   static_assert(kBatches == 2, "one batch of slots for each group of quantising warps");
@@ -185,7 +185,7 @@ __device__ __forceinline__ uint32_t quant_unit(const Unit& u, uint4& codes) {
 // and columns beyond kg of the last block are zero; scales nothing reads are
 // left as they are.
 __global__ void __launch_bounds__(256) fp8_quant_x_kernel(const uint16_t* x, int n_tok, int kg, int64_t row_len,
-                                                          int k_blocks, int sup, int tok_tiles, int tile_n, int chunks,
+                                                          int k_blocks, int sup, int tok_tiles, int tile_n,
                                                           bool aligned, uint8_t* xp, uint8_t* xsf) {
   tc::griddep_launch_dependents();                       // the product's blocks may start on their weights
   const int g = blockIdx.z, n_pad = tok_tiles * tile_n;  // a multiple of 16
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(256) fp8_quant_x_kernel(const uint16_t* x, int
   const int cols = t < n_tok ? kg - c * 16 : 0;
   const int64_t block = (int64_t)tok_tiles * tile_n * kKBlk;
   uint8_t* xd = xp + (int64_t)g * k_blocks * block + (int64_t)j * tile_n * kKBlk + code_off(r, c);
-  uint8_t* sd = xsf + ((int64_t)g * sup * tok_tiles + j) * chunks * kSfBytes + (r >> 7) * kSfBytes + scale_off(r);
-  const int64_t sf_step = (int64_t)tok_tiles * chunks * kSfBytes;
+  uint8_t* sd = xsf + ((int64_t)g * sup * tok_tiles + j) * kSfBytes + scale_off(r);
+  const int64_t sf_step = (int64_t)tok_tiles * kSfBytes;
   for (int b0 = blockIdx.y; b0 < k_blocks; b0 += 2 * gridDim.y) {
     const int b1 = b0 + gridDim.y;
     const bool two = b1 < k_blocks;
@@ -264,7 +264,6 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const uint32_t lg = (uint32_t)a.split_lg;
   const int xb = a.tile_n * kKBlk;                      // bytes of one packed activation block
-  const int n_sfb = (a.tile_n + 127) / 128;             // its scale chunks
 
   // Spread: this CTA's part of one tile.  Whole: every part of the tiles
   // blockIdx.x, blockIdx.x + gridDim.x, ...
@@ -284,9 +283,8 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
     if (tc::elect_one()) {
       // (every instruction between two blocks counts: addresses run along)
       const uint32_t sm0 = tc::smem_u32(sm), full0 = tc::smem_u32(full);
-      const uint32_t x_sf = (uint32_t)(kSfBytes * n_sfb);
-      const uint32_t bytes = (uint32_t)(kWTileBytes + (FUSE ? 0 : xb)), sf_bytes = kSfBytes + (FUSE ? 0u : x_sf);
-      const int64_t xp_step = (int64_t)a.tok_tiles * xb, xsf_step = (int64_t)a.tok_tiles * x_sf;
+      const uint32_t bytes = (uint32_t)(kWTileBytes + (FUSE ? 0 : xb)), sf_bytes = kSfBytes + (FUSE ? 0 : kSfBytes);
+      const int64_t xp_step = (int64_t)a.tok_tiles * xb, xsf_step = (int64_t)a.tok_tiles * kSfBytes;
       uint32_t x = 0, st = 0, ph = 1;                   // stages filled; the stage and its last release's phase
       const int pre = k1 - k0 < S ? k1 - k0 : S;        // blocks whose weight copies are issued ahead
       {
@@ -311,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
         const uint8_t* w = a.w + ((int64_t)rt * a.k_blocks + k0) * kWTileBytes;
         const uint8_t* wsf = a.wsf + ((int64_t)rt * a.sup + (k0 >> 2)) * kSfBytes;
         const uint8_t* xp = a.xp + ((grp * a.k_blocks + k0) * a.tok_tiles + tt) * xb;
-        const uint8_t* xsf = a.xsf + ((grp * a.sup + (k0 >> 2)) * a.tok_tiles + tt) * x_sf;
+        const uint8_t* xsf = a.xsf + ((grp * a.sup + (k0 >> 2)) * a.tok_tiles + tt) * kSfBytes;
         for (int kb = k0; kb < k1; ++kb) {
           ok = tc::mbar_wait(&empty[st], ph, kLimit);   // (a fresh barrier's wait for phase 1 passes)
           if (!ok) break;
@@ -322,7 +320,7 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
               tc::mbar_expect_tx_at(bar, bytes + sf_bytes);
               tc::bulk_g2s_at(at + kWsfOff, wsf, kSfBytes, bar);
             }
-            if (!FUSE) tc::bulk_g2s_at(at + kXsfOff, xsf, x_sf, bar);
+            if (!FUSE) tc::bulk_g2s_at(at + kXsfOff, xsf, kSfBytes, bar);
             wsf += kSfBytes;
             xsf += xsf_step;
           } else if (!ahead) {
@@ -387,17 +385,12 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
               }
               const uint32_t lo = lo0 + st * (C::kStageBytes / 16);
               const uint32_t xlo = FUSE ? slot0 + (xbatch * C::kBatch + xi) * (C::kSlotBytes / 16) : lo + kXOff / 16;
-              const uint32_t wsf = tmem + C::kWsfBase + wr * 4, xsf = tmem + C::kXsfBase + xr * 4 * C::kChunks;
+              const uint32_t wsf = tmem + C::kWsfBase + wr * 4, xsf = tmem + C::kXsfBase + xr * 4;
               const uint32_t wsf_id = wsf + ((uint32_t)id << 30), xsf_id = FUSE ? xsf : xsf + ((uint32_t)id << 30);
               const uint32_t idesc = idesc0 + id * kIdStep;
               if (sf) tc::tmem_cp_32x128b_x4(wsf, tc::desc64(lo + kWsfOff / 16, sf_hi));
-              if (FUSE || sf) {
-#pragma unroll
-                for (int ch = 0; ch < C::kChunks; ++ch)
-                  if (ch < n_sfb)
-                    tc::tmem_cp_32x128b_x4(xsf + 4 * ch,
-                                           tc::desc64(FUSE ? xlo + NT * kKBlk / 16 : lo + (kXsfOff + kSfBytes * ch) / 16, sf_hi));
-              }
+              if (FUSE || sf)
+                tc::tmem_cp_32x128b_x4(xsf, tc::desc64(FUSE ? xlo + NT * kKBlk / 16 : lo + kXsfOff / 16, sf_hi));
               tc::mma_mxf8(acc, tc::desc64(lo, desc_hi), tc::desc64(xlo, desc_hi), idesc, wsf_id, xsf_id, more);
 #pragma unroll
               for (int m = 1; m < 4; ++m)
@@ -684,7 +677,7 @@ __global__ void __launch_bounds__(256) fp8_quant_w_kernel(const uint16_t* w, int
 namespace {
 
 struct Plan {
-  int row_tiles, k_blocks, sup, splits, nt, tok_tiles, tile_n, chunks, tiles;
+  int row_tiles, k_blocks, sup, splits, nt, tok_tiles, tile_n, tiles;
   bool fuse, spread, pair;
   size_t xsf;                 // workspace offset of the tokens' scales (their codes come first)
 };
@@ -789,7 +782,6 @@ Plan fp8_plan(int n_out, int k_in, int groups, int n_tok, int sms) {
       choose_form(p, n_out, groups, n_tok, sms);
     }
   }
-  p.chunks = (p.tile_n + 127) / 128;
   p.tiles = p.row_tiles * p.tok_tiles;
   p.xsf = al256((size_t)groups * p.k_blocks * p.tok_tiles * p.tile_n * kKBlk);
   return p;
@@ -942,7 +934,7 @@ cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int group
   lc.blockDim = dim3(256);
   lc.stream = st;
   cudaError_t e = cudaLaunchKernelEx(&lc, fp8_quant_x_kernel, x, n_tok, kg, (int64_t)k_in, p.k_blocks, p.sup, p.tok_tiles,
-                                     p.tile_n, p.chunks, aligned, base, base + p.xsf);
+                                     p.tile_n, aligned, base, base + p.xsf);
   note_launch();
   if (e != cudaSuccess) return e;
   if (p.pair) {
