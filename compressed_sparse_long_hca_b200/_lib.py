@@ -79,6 +79,7 @@ SIGNATURES = {
     "csa_gemm_fp8_quant_weight": (_I32, [_P, _I32, _I32, _I32, _P, _P, _P]),
     "csa_gemm_fp8_pack_weight": (_I32, [_P, _P, _I32, _I32, _I32, _P, _SZ, _P]),
     "csa_gemm_fp8_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "csa_debug_fp8_form": (_I32, [_I32, _I32, _I32, _I32, _I32]),
     "csa_head_norm": (_I32, [_I64, _I32, _I32, ctypes.c_double, _P, _P, _P, _P, _P]),
     "csa_gemm_fp8": (_I32, [_P, _I32, _I32, _I32, _P, _I32, _I32, _P, _P, _SZ, _P]),
 }

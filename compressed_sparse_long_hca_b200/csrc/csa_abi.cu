@@ -65,6 +65,7 @@ cudaError_t launch_fp8_quant_weight(const uint16_t* w, int n_out, int k_in, int 
 cudaError_t launch_gemm_fp8(const void* w_packed, int n_out, int k_in, int groups, const uint16_t* x, int n_tok,
                             const GemmOut& out, void* ws, int sms, cudaStream_t st);
 cudaError_t fp8_read_error(int32_t* code, int32_t* detail);
+int fp8_form(int n_out, int k_in, int groups, int n_tok, int sms);
 int head_norm_max_dim();
 cudaError_t launch_head_norm(HeadNormArgs a, int sms, cudaStream_t st);
 }  // namespace csa
@@ -1002,6 +1003,13 @@ csa_status csa_gemm_check_device_error(csa_stream_t stream) {
     return fail(CSA_ERR_DEVICE_TIMEOUT, msg);
   }
   return CSA_OK;
+}
+
+int32_t csa_debug_fp8_form(int32_t n_out, int32_t k_in, int32_t groups, int32_t n_tok, int32_t sms) {
+  std::string why;
+  if (!fp8_shape_ok(n_out, k_in, groups, &why) || n_tok < 1 || n_tok > CSA_FP8_MAX_TOKENS) return 0;
+  if (sms <= 0) sms = sm_count();
+  return sms > 0 ? csa::fp8_form(n_out, k_in, groups, n_tok, sms) : 0;
 }
 
 csa_status csa_debug_wait_timeout(csa_cache_t* c, int32_t limit_us, csa_stream_t stream) {

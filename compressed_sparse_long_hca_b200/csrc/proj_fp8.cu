@@ -44,6 +44,7 @@
 
 #include <algorithm>
 
+#include "csa.h"
 #include "proj_fp8.cuh"
 #include "tc.cuh"
 
@@ -847,6 +848,12 @@ WeightLayout weight_layout(int n_out, int k_in, int groups) {
 }  // namespace
 
 size_t fp8_weight_bytes(int n_out, int k_in, int groups) { return weight_layout(n_out, k_in, groups).total; }
+
+// The kernel that a call takes (csa_debug_fp8_form).
+int fp8_form(int n_out, int k_in, int groups, int n_tok, int sms) {
+  const Plan p = fp8_plan(n_out, k_in, groups, n_tok, sms);
+  return p.pair ? 256 : p.nt | (p.spread ? CSA_FP8_FORM_CLUSTER : 0) | (p.tok_tiles > 1 ? CSA_FP8_FORM_TILES : 0);
+}
 
 // Room for the quantised tokens in every form of n_tok tokens, so that a
 // workspace for many tokens serves fewer, too: a form's last tile reaches at

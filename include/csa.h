@@ -689,6 +689,19 @@ int64_t    csa_debug_get_length(csa_cache_t* cache, int32_t layer, int32_t req);
  */
 csa_status csa_debug_wait_timeout(csa_cache_t* cache, int32_t limit_us, csa_stream_t stream);
 
+/*
+ * Test helper: the kernel that csa_gemm_fp8 takes for n_tok tokens on a device
+ * of `sms` SMs (0: the current device), so that a test of one form of the
+ * launch can say which it is there for.  Most tokens of a CTA's tile: 16 (the
+ * tokens quantised in the product), 32, 64, 128, or 256 for pairs of SMs; with
+ * CSA_FP8_FORM_CLUSTER where a cluster's CTAs take a K part each and with
+ * CSA_FP8_FORM_TILES where there are several tiles of tokens (not for pairs).
+ * 0 for a bad shape.  Host only.
+ */
+#define CSA_FP8_FORM_CLUSTER 0x1000
+#define CSA_FP8_FORM_TILES 0x2000
+int32_t    csa_debug_fp8_form(int32_t n_out, int32_t k_in, int32_t groups, int32_t n_tok, int32_t sms);
+
 #ifdef __cplusplus
 }
 #endif

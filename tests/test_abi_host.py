@@ -288,3 +288,22 @@ def test_fp8_gemm_refuses_rows_whose_blocks_cannot_be_counted(cuda_lib):
         assert cuda_lib.csa_gemm_fp8_workspace_bytes(1, k, 1, 100) == 0
         assert cuda_lib.csa_gemm_fp8_quant_weight(P, 1, k, 1, P, P, None) == -1
         assert cuda_lib.csa_gemm_fp8_pack_weight(P, P, 1, k, 1, P, 1 << 60, None) == -1
+
+
+def test_fp8_shapes_by_the_form_of_the_launch(cuda_lib):
+    """The forms that the GPU tests are there for, on a B200's 148 SMs: a
+    change of the choice makes this fail instead of leaving a form untested."""
+    from tests import fp8_forms as F
+    form = cuda_lib.csa_debug_fp8_form
+    assert {s[0] for s in F.SHAPES} == F.FORMS
+    for want, n_out, k_in, groups, n_tok in F.SHAPES:
+        assert n_tok >= 3 and n_out > 128 and k_in // groups > 256
+        assert form(n_out, k_in, groups, n_tok, 148) == want, (n_out, k_in, groups, n_tok)
+    assert form(300, 63, 1, 4, 148) == 0 and form(300, 64, 1, 0, 148) == 0
+    # no other form over the range, and the small calls need no workspace
+    import random
+    rng = random.Random(1)
+    for _ in range(4000):
+        n_out, k = int(2 ** rng.uniform(0, 17)), 8 * int(2 ** rng.uniform(0, 11))
+        n_tok = int(2 ** rng.uniform(0, 13))
+        assert form(n_out, k, 1, n_tok, 148) in F.FORMS

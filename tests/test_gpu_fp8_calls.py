@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 
 from oracle import csa_oracle as O
+from tests import fp8_forms as F
+from tests import test_gpu_fp8 as T
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +68,102 @@ def test_a_short_workspace_off_its_alignment_is_refused():
     lin = LinearFP8.quantize(w)
     lin.check_device_error()
     lin.check_device_error(torch.cuda.Stream())
+
+
+def _form_is(shape):
+    from compressed_sparse_long_hca_b200 import _lib
+    form, n_out, k_in, groups, n_tok = shape
+    if torch.cuda.get_device_properties(0).multi_processor_count != 148:
+        pytest.skip("the shapes are those of 148 SMs")
+    assert _lib.load().csa_debug_fp8_form(n_out, k_in, groups, n_tok, 0) == form
+
+
+@pytest.mark.parametrize("shape", F.SHAPES, ids=F.name)
+def test_values_that_are_not_finite_in_every_form(shape):
+    """An infinity and a NaN reach their tokens alone, a NaN weight block its
+    outputs alone; everything else keeps its bits."""
+    _form_is(shape)
+    _, n_out, k_in, groups, n_tok = shape
+    x, _, codes, scales = T._inputs(n_out, k_in, groups, n_tok, 9)
+    bad = x.clone()
+    bad[1, ::k_in // groups], bad[n_tok - 1, k_in // groups - 1::k_in // groups] = float("inf"), float("nan")
+    lin = T._linear(codes, scales, groups)
+    y, z = torch.empty((n_tok, n_out), device="cuda"), torch.empty((n_tok, n_out), device="cuda")
+    lin(x.cuda(), y)
+    lin(bad.cuda(), z)
+    assert not bool(y.isnan().any())
+    assert bool(z[1].isnan().all()) and bool(z[n_tok - 1].isnan().all())
+    z[1], z[n_tok - 1] = y[1], y[n_tok - 1]
+    assert torch.equal(y, z)
+    nan = scales.copy()
+    nan[1, 2] = 255
+    T._linear(codes, nan, groups)(x.cuda(), z)
+    assert bool(z[:, 128:256].isnan().all())
+    assert torch.equal(z[:, :128], y[:, :128]) and torch.equal(z[:, 256:], y[:, 256:])
+    lin.check_device_error()
+
+
+@pytest.mark.parametrize("shape", [s for s in F.SHAPES if s[3] == 1 and s[1] > 400], ids=F.name)
+def test_segments_that_begin_anywhere_in_every_form(shape):
+    _form_is(shape)
+    _, n_out, k_in, _, n_tok = shape
+    T.test_segments_that_begin_anywhere(n_out, k_in, n_tok)
+
+
+@pytest.mark.parametrize("shape", [s for s in F.SHAPES if s[3] == 1 and s[1] <= 400], ids=F.name)
+def test_segments_of_few_rows_in_every_form(shape):
+    """Segments of odd sizes inside one or two row tiles."""
+    _form_is(shape)
+    _, n_out, k_in, _, n_tok = shape
+    x, _, codes, scales = T._inputs(n_out, k_in, 1, n_tok, 33)
+    lin = T._linear(codes, scales)
+    y = torch.empty((n_tok, n_out), device="cuda")
+    lin(x.cuda(), y)
+    rows = [1, 33, 127, 2, 36, 3]
+    rows.append(n_out - sum(rows))
+    outs = [torch.full((n_tok + 1, r), 5.0, dtype=torch.bfloat16 if s % 2 else torch.float32, device="cuda") for s, r in enumerate(rows)]
+    lin(x.cuda(), [t[:n_tok] for t in outs])
+    for t, part in zip(outs, y.split(rows, dim=1)):
+        assert torch.equal(t[:n_tok], part.to(t.dtype)) and bool((t[n_tok] == 5).all())
+    lin.check_device_error()
+
+
+FIRST_CALLS_CAPTURED = """
+import torch
+from compressed_sparse_long_hca_b200 import _lib
+from compressed_sparse_long_hca_b200.api import LinearFP8
+from tests import fp8_forms as F
+g = torch.Generator(device="cuda").manual_seed(1)
+calls = []
+for form, n_out, k, groups, n_tok in F.SHAPES:
+    assert _lib.load().csa_debug_fp8_form(n_out, k, groups, n_tok, 0) == form
+    lin = LinearFP8.quantize(torch.randn((n_out, k // groups), generator=g, device="cuda"), groups=groups)
+    x = torch.randn((n_tok, k), generator=g, device="cuda").to(torch.bfloat16)
+    calls.append((lin, x, torch.zeros((n_tok, n_out), device="cuda")))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for lin, x, y in calls:
+        lin(x, y)
+graph.replay()
+for _, x, _ in calls:
+    x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+graph.replay()
+for lin, x, y in calls:
+    z = torch.zeros_like(y)
+    lin(x, z)
+    assert bool((z != 0).any()) and torch.equal(y, z), tuple(y.shape)
+LinearFP8.check_device_error()
+print("captured")
+"""
+
+
+def test_the_first_call_of_every_form_can_be_captured():
+    """In a process of its own: every kernel's set-up happens inside a capture,
+    and calls of all forms follow each other in one graph."""
+    import os
+    import subprocess
+    import sys
+    _form_is(F.SHAPES[0])
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
