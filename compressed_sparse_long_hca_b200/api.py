@@ -763,7 +763,7 @@ class LinearFP8:
     def __call__(self, x: torch.Tensor, outs, workspace: torch.Tensor | None = None, stream=None):
         """x: CUDA BF16 [n_tok][k_in].  outs: one tensor or a list of CUDA
         tensors [n_tok][rows_s] (BF16 or fp32, contiguous) whose rows add up
-        to n_out, as Linear's.  A call of more than 16 tokens may need scratch:
+        to n_out, as Linear's; none overlaps x.  A call of more than 16 tokens may need scratch:
         unless `workspace` is given, it takes its own from the allocator.
         Returns outs."""
         index = self._index

@@ -916,6 +916,13 @@ csa_status csa_gemm_fp8(const void* w_packed, int32_t n_out, int32_t k_in, int32
   if (reinterpret_cast<uintptr_t>(x) % 2) return fail(CSA_ERR_ARG, "x must be 2-byte aligned");
   if (reinterpret_cast<uintptr_t>(w_packed) % 16 || reinterpret_cast<uintptr_t>(workspace) % 256)
     return fail(CSA_ERR_ARG, "w_packed must be 16-byte and workspace 256-byte aligned");
+  // (a CTA quantises its tokens while others may have stored theirs)
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), x1 = x0 + (uintptr_t)n_tok * k_in * 2;
+  for (int s = 0; s < n_seg; ++s) {
+    const uintptr_t y0 = reinterpret_cast<uintptr_t>(segs[s].y);
+    if (y0 < x1 && x0 < y0 + (uintptr_t)n_tok * segs[s].rows * (segs[s].bf16 ? 2 : 4))
+      return fail(CSA_ERR_ARG, "an output segment overlaps x");
+  }
   const int sms = sm_count();
   if (sms <= 0) return fail(CSA_ERR_CUDA, "cannot query the SM count");
   const size_t need = csa::fp8_workspace_bytes(n_out, k_in, groups, n_tok, sms);

@@ -578,7 +578,8 @@ csa_status csa_gemm_check_device_error(csa_stream_t stream);
  *   csa_gemm_fp8            X device BF16 [n_tok][k_in], 0 <= n_tok <=
  *                           CSA_FP8_MAX_TOKENS; output segments as
  *                           csa_gemm_bf16 (y of an fp32 segment 4-byte, of
- *                           a BF16 segment 2-byte aligned); workspace
+ *                           a BF16 segment 2-byte aligned; none overlaps
+ *                           x, CSA_ERR_ARG); workspace
  *                           256-byte aligned, owned by the caller, not used
  *                           by other work until the call's kernels finish.
  *                           w_packed is read before the kernel queued ahead

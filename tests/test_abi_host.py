@@ -307,3 +307,17 @@ def test_fp8_shapes_by_the_form_of_the_launch(cuda_lib):
         n_out, k = int(2 ** rng.uniform(0, 17)), 8 * int(2 ** rng.uniform(0, 11))
         n_tok = int(2 ** rng.uniform(0, 13))
         assert form(n_out, k, 1, n_tok, 148) in F.FORMS
+
+
+def test_fp8_gemm_refuses_an_output_on_its_tokens(cuda_lib):
+    X, Y, n, k = 0x10000000, 0x90000000, 100, 4096
+    end = X + n * k * 2
+    seg = (_lib.GemmOut * 2)()
+    segs = ctypes.cast(seg, ctypes.c_void_p)
+    seg[0].rows, seg[0].bf16, seg[1].rows, seg[1].bf16 = 1000, 0, 1368, 1
+    for y0, y1, overlap in ((X, Y, True), (Y, X, True), (end - 4, Y, True), (X - n * 1000 * 4 + 4, Y, True), (Y, end - 2, True),
+                            (Y, X - n * 1368 * 2 + 2, True), (end, X - n * 1368 * 2, False), (X - n * 1000 * 4, end, False)):
+        seg[0].y, seg[1].y = y0, y1
+        # (without the workspace that it needs nothing is launched in any case)
+        assert cuda_lib.csa_gemm_fp8(0x10000, 2368, k, 1, X, n, 2, segs, None, 0, None) != 0
+        assert (b"overlaps" in cuda_lib.csa_last_error()) == overlap, (hex(y0), hex(y1))

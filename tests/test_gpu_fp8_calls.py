@@ -167,3 +167,15 @@ def test_the_first_call_of_every_form_can_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n_tok", [3, 40, 300])
+def test_in_place_is_refused(n_tok):
+    from compressed_sparse_long_hca_b200.api import LinearFP8
+    lin = LinearFP8.quantize(np.eye(1024, dtype=np.float32))
+    x = torch.ones((n_tok, 1024), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(RuntimeError, match="overlaps x"):
+        lin(x, x)
+    y = torch.empty_like(x)
+    lin(x, y)
+    assert torch.equal(x, y)
