@@ -918,7 +918,12 @@ class HeadNorm:
         (None when nothing is rotated).  Returns (q_out, k_out)."""
         q_out = q if q_out is None else q_out
         k_out = k if k_out is None else k_out
-        self._launch(self._checked(positions, q, q_out, k, k_out), stream)
+        n, pos, part, k_part = self._checked(positions, q, q_out, k, k_out)
+        # (_launch's body: a call less, 0.1 us of 7)
+        status = _on_device(self._index, self.lib.csa_head_norm, n, self.dim, self.rope, self.eps, pos, self._theta, part,
+                            k_part, _raw_stream(stream, self._index))
+        if status:
+            check(status, "csa_head_norm")
         return q_out, k_out
 
     def _checked(self, positions, q, q_out, k, k_out) -> tuple:
