@@ -188,8 +188,9 @@ class Cache:
         state_ready (CSA_ATTN_STATE_READY): the call directly follows this
         step's index_topk on the stream, so the lengths, window rows and q
         may be read before that kernel ends.
-        q_rotated (CSA_ATTN_Q_ROTATED): q's RoPE dims are rotated already
-        (HeadNorm)."""
+        q_rotated (CSA_ATTN_Q_ROTATED): q's RoPE dims are rotated already, at
+        the query's position with the cache's D_rope and rope_base (HeadNorm
+        of that rope and rope_base: nothing here can tell)."""
         n = req_ids.numel()
         _need(req_ids, torch.int32, name="req_ids")
         _need(q, self.qdtype, (n, self.H, self.D), "q")
@@ -969,11 +970,14 @@ class LayerProjections:
         q [n, H, D] BF16 (before RoPE), on a CSA layer q_I [n, H_I, d_I] fp32.
 
     Weights are host arrays [out, in] (rounded to BF16 when packed).  fmt:
-    "bf16" (Linear) or "fp8" (LinearFP8: half the weight bytes; the blocks of
-    128 rows are those of the two fused weights).  norm: a HeadNorm of dim D
-    that is applied in place after the products, to every head of q (with its
-    rotation) and to c; the attention then takes q with q_rotated=True (when
-    the norm's rope is not 0)."""
+    "bf16" (Linear) or "fp8" (LinearFP8: half the weight bytes).  The blocks
+    of 128 rows are then those of the two fused weights, quantised here: a
+    part may begin inside one, so codes that were quantised part by part
+    cannot be taken over (LinearFP8 itself takes codes).  norm: a HeadNorm of
+    dim D that is applied in place after the products, to every head of q
+    (with its rotation) and to c, the candidate that the append pools; the
+    attention then takes q with q_rotated=True (when the norm's rope is not
+    0).  Its rope and rope_base are to be the cache's."""
 
     def __init__(self, *, csa: bool, W_c, W_z, W_dq, W_uq, W_cI=None, W_zI=None, W_w=None, W_uqI=None,
                  device: str | torch.device = "cuda", fmt: str = "bf16", norm: HeadNorm | None = None):

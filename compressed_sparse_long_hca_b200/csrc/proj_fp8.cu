@@ -39,7 +39,7 @@
 // straight into the MMA's operand layout.  Beyond that the quantised tokens
 // are worth keeping: a kernel packs them once, and the product's CTAs read
 // blocks of them by bulk copies (7168 x 16384, 37 tokens: 46 us with the
-// tokens quantised in every CTA, 29 us packed; 20 tokens 34 and 26 us).
+// tokens quantised in every CTA, 26 us packed).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -402,9 +402,11 @@ __global__ void __launch_bounds__(Cfg<NT, FUSE, ONE>::kThreads, Cfg<NT, FUSE, ON
               if (kb == b1) tc::mma_commit(&acc_full[u & kAccMask]);
               if (FUSE) {
                 xr = (xr + 1) & (C::kXsfRing - 1);
-                // (the batch is counted, not derived from a slot number: with
+                // (The batch is counted, not derived from a slot number.  With
                 // x_empty[slot / 4] under slot % 4 == 3 this commit faulted on
-                // a misaligned barrier address)
+                // a misaligned address, though by the source that address is
+                // aligned for every slot: the cause is not known, and that
+                // form is not used.)
                 if (++xi == C::kBatch) {
                   tc::mma_commit(&x_empty[xbatch]);
                   xi = 0;
@@ -689,7 +691,8 @@ size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 // power of two that gives the SMs two CTAs each, every part at least
 // kMinPartBlocks blocks long; 7/8 of the places count, for a cluster lies
 // within a group of 16 to 20 SMs and those are not filled to the last place
-// (56 clusters of 5 ran as two waves: 40 us instead of 26).
+// (7168 x 16384, 37 tokens: 56 clusters of 5 ran as two waves, 40 us; clusters of
+// 4 take 26).
 int fp8_splits(int row_tiles, int k_blocks, int sms) {
   int s = 1;
   while (2 * s <= kMaxParts && 16 * s * row_tiles <= 14 * sms && 2 * s * kMinPartBlocks <= k_blocks) s *= 2;
@@ -712,14 +715,14 @@ bool fp8_fused(int row_tiles, int k_blocks, int splits, int n_tok, int sms) {
 // CTA per part of a tile, and the tokens of a tile.  Each has an estimated time,
 // waves x (K blocks x time of a block + time of a tile's end), and the least is
 // taken; the constants (microseconds) are fits to measured calls:
-//   639 x 750 x 8496      whole, 32 tokens a tile 22.3   parts, 128 tokens 17.0
-//   140 x 1624 x 5320     whole, 80 tokens 16.4          parts, 96 tokens 11.3
-//   905 x 89 x 12512      whole, 32 tokens 30.0          parts, 64 tokens 15.4
-//   128 x 9000 x 2048     parts, 128 tokens 15.6         whole, 64 tokens 9.5
-//   160 x 7168 x 16384    pairs 41.9                     whole, 80 tokens 36.9
-//   256 x 24576 x 1536    whole, 128 tokens 17.1         pairs 15.2
-//   2754 x 2564 x 488     whole, 128 tokens 15.5         pairs 12.7
-//   595 x 8875 x 1224     pairs 21.9                     whole, 128 tokens 15.4
+//   639 x 750 x 8496      whole, 32 tokens a tile 22.3   parts, 128 tokens 16.8
+//   140 x 1624 x 5320     whole, 80 tokens 16.4          parts, 96 tokens 10.9
+//   905 x 89 x 12512      whole, 32 tokens 30.0          parts, 64 tokens 15.5
+//   128 x 9000 x 2048     parts, 128 tokens 15.6         whole, 64 tokens 9.4
+//   160 x 7168 x 16384    pairs 41.9                     whole, 80 tokens 36.0
+//   256 x 24576 x 1536    whole, 128 tokens 17.1         pairs 16.0
+//   2754 x 2564 x 488     whole, 128 tokens 15.5         pairs 12.6
+//   595 x 8875 x 1224     pairs 21.9                     whole, 128 tokens 15.5
 // A pair stores output rows that are not on 32 bytes more slowly, and odd ones
 // more slowly still; the plan, which does not know the outputs, takes the row
 // length for that.
